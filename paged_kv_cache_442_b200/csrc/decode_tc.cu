@@ -1225,6 +1225,12 @@ __global__ void __launch_bounds__(kThreadsOf<G, F8>, 1) decode_tc_kernel(
           // V rows past the partition's end may hold anything (even NaN); P is 0 there
           // but 0 * NaN is NaN: clear them before the tensor core reads the tile
           const int vs = j % NV;
+          // A parity wait is only sound once the phase before it is known to be complete.
+          // The P buffer's wait above covers V tile j - NP, which is older than this
+          // slot's last one (j - NV): a V load slower than the score path would make the
+          // wait below pass at once, clear the older tile and leave this one's rows.
+          if (j >= NV)
+            failed |= !wait_or_abort(&v_full[vs], ((j / NV) - 1) & 1, p.err, abort_flag, wl);
           failed |= !wait_or_abort(&v_full[vs], (j / NV) & 1, p.err, abort_flag, wl);
 #pragma unroll
           for (int u = 0; u < SUB; ++u) {
