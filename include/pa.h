@@ -34,9 +34,9 @@
  * ------
  *  - Arguments are validated on the host before any launch; a bad argument
  *    returns PA_ERR_INVALID_ARG and launches nothing. Supported sizes:
- *    head_dim 64 or 128 for the store, copy and decode entry points, 128 only
- *    for pa_prefill, pa_store_prefill and pa_decode_fp8 (other head dims
- *    return PA_ERR_UNSUPPORTED there); block_size a power of two in
+ *    head_dim 64 or 128 for the store, copy, rotary and decode entry points, 128
+ *    only for pa_prefill, pa_store_prefill, pa_decode_fp8 and
+ *    pa_decode_fp8_blockscale (other head dims return PA_ERR_UNSUPPORTED there); block_size a power of two in
  *    [16, 1024]; num_q_heads a multiple of num_kv_heads.
  *  - A valid but unimplemented combination returns PA_ERR_UNSUPPORTED.
  *  - A failed launch returns PA_ERR_CUDA.
@@ -415,6 +415,155 @@ pa_status pa_decode_fp8(void* out, const void* q, const void* k_codes, const voi
                         const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
                         float scale, int32_t max_context_len, int32_t partition_size,
                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions. A head's first rot_dim dims form rot_dim / 2 pairs; pair i of a token
+ * at position p is turned by the angle t = p * inv_freq[i]:
+ *     a' = amplitude (a cos t - b sin t),   b' = amplitude (b cos t + a sin t),
+ * the dims past rot_dim are copied. Half layout: the pair is (i, i + rot_dim / 2);
+ * interleaved: (2 i, 2 i + 1). inv_freq is taken as the exact number its fp32 holds; the
+ * angle is reduced to less than a turn in 64 bits, so far positions lose nothing; products
+ * are fp32, rounded once to bf16. Positions are any int32 (they need not be the cache's
+ * row numbers: a sequence that dropped its oldest blocks goes on counting).
+ */
+typedef struct {
+  const float* inv_freq; /* device, fp32 [rot_dim / 2]                              */
+  int32_t rot_dim;       /* even, 0 .. head_dim (0: nothing is rotated)             */
+  int32_t interleaved;   /* 0: half layout, 1: interleaved                          */
+  float amplitude;       /* factor of the rotated dims (1 unless scaled, see below) */
+} pa_rope_desc;
+
+/* How pa_rope_inv_freq stretches the frequencies base^(-2 i / rot_dim) for contexts longer
+ * than those a model was trained on. */
+typedef enum {
+  PA_ROPE_PLAIN = 0,  /* unchanged                                                       */
+  PA_ROPE_LINEAR = 1, /* every frequency / factor                                        */
+  PA_ROPE_BASE = 2,   /* base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is     */
+                      /* stretched by factor, the fastest not at all                     */
+  PA_ROPE_RAMP = 3    /* pairs that turn more than beta_fast times within                */
+                      /* original_context stay, those below beta_slow turns are divided  */
+                      /* by factor, a linear ramp over the pair index between; amplitude  */
+                      /* 1 + 0.1 ln(factor)                                              */
+} pa_rope_scaling;
+
+/*
+ * pa_rope_inv_freq — the frequency table of a rotary embedding (host memory, no CUDA call):
+ * inv_freq_out fp32 [rot_dim / 2], computed in 64 bits and rounded once; *amplitude_out
+ * (may be NULL) the factor for pa_rope_desc. rot_dim even and > 0 (> 2 for PA_ROPE_BASE),
+ * base > 1, factor >= 1; PA_ROPE_RAMP also needs original_context > 0 and
+ * beta_fast > beta_slow > 0. Arguments a mode does not use are ignored.
+ */
+pa_status pa_rope_inv_freq(float* inv_freq_out, float* amplitude_out, int32_t rot_dim, double base,
+                           pa_rope_scaling scaling, double factor, double original_context,
+                           double beta_fast, double beta_slow);
+
+/*
+ * pa_rope — rotate the heads of x: out[t, h] = x[t, h] turned by positions[t].
+ *   out, x      bf16 rows of num_heads * head_dim values, x_stride / out_stride elements
+ *               between tokens (a slice of a fused projection is passed as it is). out may
+ *               be x with the same stride; any other overlap is a caller error.
+ *   positions   int32 [num_tokens], device.
+ * head_dim 64 or 128; strides multiples of 8, at least num_heads * head_dim; 16-byte
+ * aligned pointers. rot_dim multiples of 16 take the vectorised path.
+ */
+pa_status pa_rope(void* out, int64_t out_stride, const void* x, int64_t x_stride,
+                  int32_t num_tokens, int32_t num_heads, int32_t head_dim,
+                  const int32_t* positions, pa_rope_desc rope, void* stream);
+
+/*
+ * pa_rope_store_kvcache — rotate the step's queries and keys and store the keys and values
+ * in one pass: q_out = pa_rope(q), then pa_store_kvcache(pa_rope(k), v), with the same bits.
+ *   q, q_out      [num_tokens, num_q_heads, D], strides as in pa_rope (q_out may be q);
+ *                 num_q_heads 0: no queries (both NULL).
+ *   k, v          [num_tokens, Hkv, D], read only.
+ *   slot_mapping  as in pa_store_kvcache (-1 skips the token's k and v; its q is rotated).
+ */
+pa_status pa_rope_store_kvcache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                void* k_cache, void* v_cache, pa_cache_desc cache,
+                                const int32_t* slot_mapping, int32_t num_tokens,
+                                int32_t num_q_heads, const int32_t* positions, pa_rope_desc rope,
+                                void* stream);
+
+/*
+ * e4m3 KV cache with block scales: one fp32 scale for each (block, kv head) of K and of V
+ * instead of one per row (pa_store_kvcache_fp8): codes uint8 [num_blocks, block_size, Hkv, D],
+ * scales fp32 [num_blocks, Hkv]. A stored value reads back as e4m3(code) * scale.
+ *
+ * A block fills row by row, so its scale follows its rows:
+ *  - a row at offset 0 starts the block afresh (whatever codes and scale it held);
+ *  - scale = the smallest power of two >= 2^-126 with |x| <= 448 * scale for every finite
+ *    value of the rows written so far; it never shrinks until the block starts afresh;
+ *  - code = e4m3(x / scale), nearest even, saturated to +-448 (infinities too; NaN stays);
+ *  - when later rows make a scale grow, the rows already there are requantised,
+ *    code' = e4m3(value(code) * old / new). A power of two only moves e4m3 exponents, so
+ *    this rounds only what falls below 2^-6 of the new scale (in steps of 2^-9 of it).
+ */
+
+/*
+ * pa_store_kvcache_fp8_blockscale — append each sequence's new rows to such pools. New token
+ * i of sequence s (rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] - 1 of k and v) goes to
+ * position context_lens[s] - n_new + i through the block table (the token order of
+ * pa_prefill; a decode step has cu_seqlens_q = 0, 1, 2, ...).
+ *   k, v            bf16 [num_tokens, Hkv, D], strides as in pa_rope.
+ *   cu_seqlens_q    int32 [num_seqs + 1], device; context_lens int32 [num_seqs], including
+ *                   the new tokens.
+ *   max_q_len       host upper bound of the new tokens of one sequence.
+ * No two sequences of a call may append to one block, and a block that other sequences read
+ * is copied first (copy-on-write). Rows past the new ones stay as they are. A sequence whose
+ * lengths do not fit (n_new above context_lens, max_q_len or num_tokens, a context past the
+ * table) is skipped, as is a block with a bad id; both are reported as PA_ERR_BAD_INDEX.
+ * head_dim 64 or 128. Deterministic (no atomics).
+ */
+pa_status pa_store_kvcache_fp8_blockscale(const void* k, int64_t k_stride, const void* v,
+                                          int64_t v_stride, void* k_codes, void* v_codes,
+                                          float* k_scales, float* v_scales, pa_cache_desc cache,
+                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* cu_seqlens_q, const int32_t* context_lens,
+                                          int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
+                                          void* stream);
+
+/*
+ * pa_rope_store_kvcache_fp8_blockscale — q_out = pa_rope(q), then
+ * pa_store_kvcache_fp8_blockscale(pa_rope(k), v), in one launch and with the same bits.
+ * positions int32 [num_tokens]; q, q_out and num_q_heads as in pa_rope_store_kvcache.
+ * rot_dim must be a multiple of 16 (else PA_ERR_UNSUPPORTED: use the two calls).
+ */
+pa_status pa_rope_store_kvcache_fp8_blockscale(
+    void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+    int64_t k_stride, const void* v, int64_t v_stride, void* k_codes, void* v_codes,
+    float* k_scales, float* v_scales, pa_cache_desc cache, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q, const int32_t* context_lens,
+    int32_t num_seqs, int32_t num_tokens, int32_t max_q_len, int32_t num_q_heads,
+    const int32_t* positions, pa_rope_desc rope, void* stream);
+
+/*
+ * pa_decode_fp8_blockscale — pa_decode over e4m3 pools with block scales: one query token
+ * per sequence attends over the values the pools hold (code * scale; scales any finite
+ * fp32 >= 0). The tensor cores read the codes as they are stored; q reaches them as three
+ * e4m3 terms (about 2^-13 relative per element), the probabilities, times their block's V
+ * scale over the largest one of the part, as two (about 2^-8 relative; below 2^-10 of the
+ * part's largest product of probability and V scale the error is absolute, about 2^-18 of
+ * it). The context is split over the SMs evenly, whatever the lengths; no partition size.
+ *   out, q          [num_seqs, Hq, D] bf16; a sequence with context_lens[s] <= 0 gets zeros.
+ *   max_context_len host upper bound of context_lens; a larger device value is clipped to
+ *                   it and reported as PA_ERR_BAD_INDEX.
+ *   workspace       16-byte aligned device scratch of at least
+ *                   pa_decode_fp8_blockscale_workspace_size bytes; contents on entry do not
+ *                   matter. Calls that overlap on the GPU must use different ones. A call
+ *                   captured into a CUDA graph replays as it is (its counters are left
+ *                   ready; only after a call that timed out must the workspace be cleared
+ *                   before such a replay).
+ * Supported: head_dim 128, Hq / Hkv in {1, 2, 4, 8, 16}; else PA_ERR_UNSUPPORTED.
+ */
+size_t pa_decode_fp8_blockscale_workspace_size(int32_t num_q_heads, int32_t num_kv_heads);
+pa_status pa_decode_fp8_blockscale(void* out, const void* q, const void* k_codes,
+                                   const void* v_codes, const float* k_scales,
+                                   const float* v_scales, pa_cache_desc cache,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, int32_t num_seqs,
+                                   int32_t num_q_heads, float scale, int32_t max_context_len,
+                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * pa_prefill — causal attention of a chunk of new tokens appended to each

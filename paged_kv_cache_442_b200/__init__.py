@@ -25,7 +25,10 @@ EXPORTED = ("pa_bm_create", "pa_bm_destroy", "pa_bm_allocate", "pa_bm_allocate_b
             "pa_store_kvcache", "pa_copy_blocks", "pa_decode_default_partition", "pa_decode_workspace_size",
             "pa_decode", "pa_store_decode", "pa_decode_shared_prefix",
             "pa_decode_shared_prefix_workspace_size", "pa_decode_no_alloc", "pa_prefill", "pa_store_prefill",
-            "pa_store_kvcache_fp8", "pa_decode_fp8", "pa_set_debug_checks", "pa_set_wait_limit_ns",
+            "pa_store_kvcache_fp8", "pa_decode_fp8", "pa_rope_inv_freq", "pa_rope",
+            "pa_rope_store_kvcache", "pa_store_kvcache_fp8_blockscale",
+            "pa_rope_store_kvcache_fp8_blockscale", "pa_decode_fp8_blockscale_workspace_size",
+            "pa_decode_fp8_blockscale", "pa_set_debug_checks", "pa_set_wait_limit_ns",
             "pa_check_device_errors", "pa_status_string", "pa_version")
 
 # size of the library-owned scratch of pa_decode_no_alloc (include/pa.h)
@@ -42,6 +45,14 @@ class pa_cache_desc(ctypes.Structure):
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
+
+class pa_rope_desc(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float)]
+
+
+# pa_rope_scaling
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 
 _lib = None
 
@@ -109,6 +120,26 @@ def load_library(path: str | None = None):
     lib.pa_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, pa_cache_desc, vp, i32, vp, i32, i32,
                                   ctypes.c_float, i32, i32, vp, sz, vp]
     lib.pa_decode_fp8.restype = ctypes.c_int
+    i64, f64 = ctypes.c_int64, ctypes.c_double
+    lib.pa_rope_inv_freq.argtypes = [vp, vp, i32, f64, ctypes.c_int, f64, f64, f64, f64]
+    lib.pa_rope_inv_freq.restype = ctypes.c_int
+    lib.pa_rope.argtypes = [vp, i64, vp, i64, i32, i32, i32, vp, pa_rope_desc, vp]
+    lib.pa_rope.restype = ctypes.c_int
+    lib.pa_rope_store_kvcache.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, pa_cache_desc,
+                                          vp, i32, i32, vp, pa_rope_desc, vp]
+    lib.pa_rope_store_kvcache.restype = ctypes.c_int
+    lib.pa_store_kvcache_fp8_blockscale.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, pa_cache_desc,
+                                                    vp, i32, vp, vp, i32, i32, i32, vp]
+    lib.pa_store_kvcache_fp8_blockscale.restype = ctypes.c_int
+    lib.pa_rope_store_kvcache_fp8_blockscale.argtypes = [
+        vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, pa_cache_desc, vp, i32, vp, vp, i32, i32,
+        i32, i32, vp, pa_rope_desc, vp]
+    lib.pa_rope_store_kvcache_fp8_blockscale.restype = ctypes.c_int
+    lib.pa_decode_fp8_blockscale_workspace_size.argtypes = [i32, i32]
+    lib.pa_decode_fp8_blockscale_workspace_size.restype = sz
+    lib.pa_decode_fp8_blockscale.argtypes = [vp, vp, vp, vp, vp, vp, pa_cache_desc, vp, i32, vp, i32,
+                                             i32, ctypes.c_float, i32, vp, sz, vp]
+    lib.pa_decode_fp8_blockscale.restype = ctypes.c_int
     lib.pa_set_debug_checks.argtypes = [ctypes.c_int]
     lib.pa_set_debug_checks.restype = None
     lib.pa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -278,6 +309,230 @@ def pa_decode_fp8(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, co
                            _ptr(workspace) if workspace is not None else ctypes.c_void_p(0),
                            ws_bytes, _stream(stream))
     _raise("pa_decode_fp8", st)
+
+
+def _rows(t, name, num_tokens=None, shape=None):
+    """A bf16 CUDA tensor [tokens, heads, dim] whose tokens' rows are dense (the tokens may be
+    any multiple of 8 values apart: a slice of a fused projection). Returns its token stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
+    if (num_tokens is not None and t.shape[0] != num_tokens) or \
+            (shape is not None and tuple(t.shape[1:]) != tuple(shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"[{num_tokens if num_tokens is not None else 'tokens'}, "
+                         f"{', '.join(map(str, shape)) if shape is not None else 'heads, dim'}]")
+    heads, dim = t.shape[1], t.shape[2]
+    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return int(t.stride(0)) if t.shape[0] > 1 else -(-heads * dim // 8) * 8
+
+
+def _rope_desc(inv_freq, interleaved, amplitude):
+    torch = _torch()
+    _check(inv_freq, "inv_freq", torch.float32, 1)
+    return pa_rope_desc(inv_freq.data_ptr() if inv_freq.numel() else None,
+                        2 * int(inv_freq.shape[0]), 1 if interleaved else 0, float(amplitude))
+
+
+def _same_device(*tensors):
+    """Tensors of one call live on the current device (its kernels and scratch belong to it)."""
+    torch = _torch()
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+def pa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original_context: float = 0.0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0):
+    """Frequency table of a rotary embedding: (list of rot_dim / 2 floats, amplitude). scaling
+    stretches it for longer contexts: "linear", "base" or "ramp" (include/pa.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    table = (ctypes.c_float * max(1, int(rot_dim) // 2))()
+    amplitude = ctypes.c_float(1.0)
+    st = load_library().pa_rope_inv_freq(table, ctypes.byref(amplitude), int(rot_dim), float(base),
+                                         ROPE_SCALINGS[scaling], float(factor),
+                                         float(original_context), float(beta_fast),
+                                         float(beta_slow))
+    _raise("pa_rope_inv_freq", st)
+    return list(table), amplitude.value
+
+
+def pa_rope(out, x, positions, inv_freq, interleaved: bool = False, amplitude: float = 1.0,
+            stream=None) -> None:
+    """out[t, h] = x[t, h] turned by positions[t] (out may be x): the first
+    2 * len(inv_freq) dims of each head, the others copied. Tokens may be strided."""
+    torch = _torch()
+    lib = load_library()
+    xs = _rows(x, "x")
+    T, H, D = x.shape
+    os_ = _rows(out, "out", T, (H, D))
+    _check(positions, "positions", torch.int32, 1)
+    if positions.shape[0] != T:
+        raise ValueError("positions must be [num_tokens]")
+    rope = _rope_desc(inv_freq, interleaved, amplitude)
+    _same_device(out, x, positions, inv_freq)
+    st = lib.pa_rope(_ptr(out), os_, _ptr(x), xs, int(T), int(H), int(D), _ptr(positions), rope,
+                     _stream(stream))
+    _raise("pa_rope", st)
+
+
+def _rope_step_rows(q_out, q, k, v, kv_shape):
+    """Token strides of (q_out, q, k, v) and the number of query heads (0 without queries)."""
+    ks = _rows(k, "k", None, kv_shape)
+    T = k.shape[0]
+    vs = _rows(v, "v", T, kv_shape)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is None:
+        return 0, 0, ks, vs, 0
+    qs = _rows(q, "q", T)
+    if q.shape[2] != kv_shape[1]:
+        raise ValueError("q and k must have the same head dim")
+    return _rows(q_out, "q_out", T, tuple(q.shape[1:])), qs, ks, vs, int(q.shape[1])
+
+
+def pa_rope_store_kvcache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                          interleaved: bool = False, amplitude: float = 1.0, stream=None) -> None:
+    """q_out = rotated q; rotated k and v stored at slot_mapping (-1 skips): one launch. q, k
+    and v may be slices of one projection; q_out may be q; q and q_out may be None."""
+    torch = _torch()
+    lib = load_library()
+    _check(k_cache, "k_cache", torch.bfloat16, 4)
+    _check(v_cache, "v_cache", torch.bfloat16, 4)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache/v_cache shapes must match")
+    qos, qs, ks, vs, hq = _rope_step_rows(q_out, q, k, v, tuple(k_cache.shape[2:]))
+    _check(slot_mapping, "slot_mapping", torch.int32, 1)
+    _check(positions, "positions", torch.int32, 1)
+    T = int(k.shape[0])
+    if slot_mapping.shape[0] != T or positions.shape[0] != T:
+        raise ValueError("slot_mapping and positions must be [num_tokens]")
+    rope = _rope_desc(inv_freq, interleaved, amplitude)
+    _same_device(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq)
+    st = lib.pa_rope_store_kvcache(_ptr(q_out), qos, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+                                   _ptr(k_cache), _ptr(v_cache), cache_desc(k_cache),
+                                   _ptr(slot_mapping), T, hq, _ptr(positions), rope,
+                                   _stream(stream))
+    _raise("pa_rope_store_kvcache", st)
+
+
+def _check_blockscale_pools(torch, k_codes, v_codes, k_scales, v_scales):
+    _check(k_codes, "k_codes", torch.uint8, 4)
+    _check(v_codes, "v_codes", torch.uint8, 4)
+    _check(k_scales, "k_scales", torch.float32, 2)
+    _check(v_scales, "v_scales", torch.float32, 2)
+    nb, _, hkv, _ = k_codes.shape
+    if k_codes.shape != v_codes.shape:
+        raise ValueError("K and V pools must have the same shapes")
+    if tuple(k_scales.shape) != (nb, hkv) or tuple(v_scales.shape) != (nb, hkv):
+        raise ValueError("scales must be [num_blocks, num_kv_heads] fp32")
+
+
+def _check_new_tokens(torch, T, block_tables, cu_seqlens_q, context_lens):
+    _check(block_tables, "block_tables", torch.int32, 2)
+    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _check(context_lens, "context_lens", torch.int32, 1)
+    B = context_lens.shape[0]
+    if cu_seqlens_q.shape[0] != B + 1 or block_tables.shape[0] != B:
+        raise ValueError("cu_seqlens_q/block_tables/context_lens disagree on num_seqs")
+    return int(B)
+
+
+def pa_store_kvcache_fp8_blockscale(k, v, k_codes, v_codes, k_scales, v_scales, block_tables,
+                                    cu_seqlens_q, context_lens, max_q_len: int,
+                                    stream=None) -> None:
+    """Append each sequence's new rows (the last ones of its context) to e4m3 pools with one
+    fp32 scale per (block, kv head): codes uint8 [num_blocks, bs, Hkv, D], scales fp32
+    [num_blocks, Hkv]. A block's scale grows with its rows (include/pa.h)."""
+    torch = _torch()
+    lib = load_library()
+    _check_blockscale_pools(torch, k_codes, v_codes, k_scales, v_scales)
+    _, _, ks, vs, _ = _rope_step_rows(None, None, k, v, tuple(k_codes.shape[2:]))
+    T = int(k.shape[0])
+    B = _check_new_tokens(torch, T, block_tables, cu_seqlens_q, context_lens)
+    _same_device(k, v, k_codes, v_codes, k_scales, v_scales, block_tables, cu_seqlens_q,
+                 context_lens)
+    st = lib.pa_store_kvcache_fp8_blockscale(
+        _ptr(k), ks, _ptr(v), vs, _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales),
+        cache_desc(k_codes), _ptr(block_tables), int(block_tables.shape[1]), _ptr(cu_seqlens_q),
+        _ptr(context_lens), B, T, int(max_q_len), _stream(stream))
+    _raise("pa_store_kvcache_fp8_blockscale", st)
+
+
+def pa_rope_store_kvcache_fp8_blockscale(q_out, q, k, v, k_codes, v_codes, k_scales, v_scales,
+                                         block_tables, cu_seqlens_q, context_lens, max_q_len: int,
+                                         positions, inv_freq, interleaved: bool = False,
+                                         amplitude: float = 1.0, stream=None) -> None:
+    """q_out = rotated q, then pa_store_kvcache_fp8_blockscale of the rotated k and of v: one
+    launch, the same bits."""
+    torch = _torch()
+    lib = load_library()
+    _check_blockscale_pools(torch, k_codes, v_codes, k_scales, v_scales)
+    qos, qs, ks, vs, hq = _rope_step_rows(q_out, q, k, v, tuple(k_codes.shape[2:]))
+    T = int(k.shape[0])
+    B = _check_new_tokens(torch, T, block_tables, cu_seqlens_q, context_lens)
+    _check(positions, "positions", torch.int32, 1)
+    if positions.shape[0] != T:
+        raise ValueError("positions must be [num_tokens]")
+    rope = _rope_desc(inv_freq, interleaved, amplitude)
+    _same_device(q_out, q, k, v, k_codes, v_codes, k_scales, v_scales, block_tables, cu_seqlens_q,
+                 context_lens, positions, inv_freq)
+    st = lib.pa_rope_store_kvcache_fp8_blockscale(
+        _ptr(q_out), qos, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(k_codes), _ptr(v_codes),
+        _ptr(k_scales), _ptr(v_scales), cache_desc(k_codes), _ptr(block_tables),
+        int(block_tables.shape[1]), _ptr(cu_seqlens_q), _ptr(context_lens), B, T, int(max_q_len),
+        hq, _ptr(positions), rope, _stream(stream))
+    _raise("pa_rope_store_kvcache_fp8_blockscale", st)
+
+
+def pa_decode_fp8_blockscale_workspace_size(num_q_heads: int, num_kv_heads: int) -> int:
+    return int(load_library().pa_decode_fp8_blockscale_workspace_size(num_q_heads, num_kv_heads))
+
+
+def decode_fp8_blockscale_workspace(num_seqs, num_q_heads, num_kv_heads, device="cuda"):
+    """Allocate (with torch) the scratch pa_decode_fp8_blockscale needs. Its size depends on
+    the heads and the GPU only, so one serves batches of any size and length."""
+    torch = _torch()
+    nbytes = pa_decode_fp8_blockscale_workspace_size(num_q_heads, num_kv_heads)
+    return torch.empty(max(nbytes, 16) // 4, dtype=torch.float32, device=device)
+
+
+def pa_decode_fp8_blockscale(out, q, k_codes, v_codes, k_scales, v_scales, block_tables,
+                             context_lens, scale: float, max_context_len: int, workspace,
+                             stream=None) -> None:
+    """Paged decode attention over e4m3 pools with block scales into `out` [num_seqs, Hq, D]
+    (bf16). workspace: decode_fp8_blockscale_workspace."""
+    torch = _torch()
+    lib = load_library()
+    _check(out, "out", torch.bfloat16, 3)
+    _check(q, "q", torch.bfloat16, 3)
+    _check_blockscale_pools(torch, k_codes, v_codes, k_scales, v_scales)
+    _check(block_tables, "block_tables", torch.int32, 2)
+    _check(context_lens, "context_lens", torch.int32, 1)
+    B, Hq, D = q.shape
+    if tuple(out.shape) != (B, Hq, D) or block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("out/q/block_tables/context_lens disagree on num_seqs")
+    if D != k_codes.shape[3]:
+        raise ValueError("q and the pools must have the same head dim")
+    _check(workspace, "workspace", workspace.dtype)
+    _same_device(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens,
+                 workspace)
+    st = lib.pa_decode_fp8_blockscale(
+        _ptr(out), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales),
+        cache_desc(k_codes), _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens),
+        int(B), int(Hq), float(scale), int(max_context_len), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _raise("pa_decode_fp8_blockscale", st)
 
 
 class BlockManager:

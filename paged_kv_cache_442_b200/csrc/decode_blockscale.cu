@@ -1,0 +1,1084 @@
+// Paged decode attention over e4m3 pools with one scale per (block, kv head), on the tcgen05
+// tensor cores (head dim 128), persistent, with the work split evenly ahead of time.
+//
+// Mathematics. For a query head with kv head g and position j in block b:
+//   x_j = scale * log2(e) * ks[b] * (q . code_k,j),   out = sum_j 2^(x_j - m) vs[b] code_v,j / l,
+//   l = sum_j 2^(x_j - m). The tensor cores multiply the stored codes themselves
+//   (kind::f8f6f4, fp32 accumulation): S = K Q^T per 128 positions (M = positions, N = rows
+//   of q terms) and O^T += V^T P^T (M = head dims, N = rows of P terms).
+//   * q (bf16) is three e4m3 terms of one fp32 scale per head, y = q * 448 / amax:
+//     hi = e4m3(y), mid = e4m3(y - hi), lo = e4m3(y - hi - mid) (about 2^-13 of an element;
+//     a score's error enters the exponent multiplied by the score's size). Row 3h + t of the
+//     B operand is term t of head h, so a softmax thread reads its 3 G columns in one load.
+//   * the V scale of a block multiplies its probabilities: P'_j = 2^(x_j - m) vs[b] / R, with
+//     R the largest V scale of the item so far (kept by the scheduler warp): one exponential
+//     per (position, head). P' <= 2^kBound; a tile whose maximum would pass it moves the
+//     reference m, and a larger V scale moves R; both rescale O^T in tensor memory.
+//     P' is two e4m3 terms, hi = e4m3(P') and lo = e4m3(128 (P' - hi)) in rows 2h and 2h + 1
+//     (about 2^-8 relative, with an absolute floor of 2^-18 against a largest P' of 2^3 to
+//     2^6); O = (O_hi + O_lo / 128) R / l.
+//
+// Work. Unit = a tile of 256 positions of one (sequence, kv head). CTAs work in groups of
+// 4, 2 or 1 (the largest that divides the kv heads): the members of a group walk the same
+// tiles for neighbouring kv heads, so rows of several heads (128 bytes each) are fetched
+// together. All (sequence, head group, tile) units in order are cut into equal runs, one per
+// group: every CTA ends at the same time, and a CTA takes at most two partial (sequence,
+// kv head) items (its first and its last). The CTA that completes the last part of an item
+// merges them, sixteen parts at a time.
+//
+// Bound: HBM (every K/V code is read once). Roles, as in the bf16 decode but streaming whole
+// runs: warps 0-7 softmax (two groups, one position of a 256-position tile per thread),
+// 8-11 epilogue, 12 TMA producer, 13 tensor-core issuer, 14 scheduler. The scheduler
+// publishes each tile's block ids and scales through a ring of tile records.
+//
+// Waits name an mbarrier phase by its parity, so a wait for phase n must know that phase
+// n - 1 is complete. Every ring here is waited on phase after phase by the same role; the
+// one exception, the softmax clearing V rows, holds because NP <= NV (the P buffer's wait
+// covers the V slot's previous tile).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cfloat>
+
+#include "decode_common.cuh"
+#include "pa_internal.h"
+#include "pa_ptx.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int TT = 256;        // positions per tile
+constexpr int TM = 128;        // positions per product
+constexpr int HD = 128;        // head dim
+constexpr int NK = 3;          // K ring (tiles of 32 KB)
+constexpr int NV = 3;          // V ring
+constexpr int ND = 8;          // tile records ahead
+constexpr int QN = 2;          // q slots (one per item in flight)
+constexpr int NO = 2;          // O^T accumulators
+constexpr int kMaxBlk = 16;    // blocks of one tile (block size 16)
+constexpr int kTileBytes = TT * HD;
+constexpr int kHalf = TM * HD;
+constexpr int kThreads = 480;
+constexpr int kSoftThreads = 256;
+constexpr int kFan = 16;       // parts merged at a time
+constexpr float kTarget = 3.f;  // a new reference puts the largest P' at 2^kTarget ...
+constexpr float kBound = 6.f;   // ... and it moves when one would pass 2^kBound (128 (P' - hi)
+                                // is then at most 256, inside e4m3's 448)
+constexpr float kLoScale = 128.f;
+constexpr float kLog2eF = 1.4426950408889634f;
+
+constexpr int round_up(int x, int a) { return (x + a - 1) / a * a; }
+
+struct TileRec {
+  int ids[kMaxBlk];
+  float ks[kMaxBlk];
+  float vs[kMaxBlk];   // V scale / R
+  int n;               // positions of the tile inside the context
+  int first;           // first tile of its item
+  int last;            // last tile of its item
+  int stop;            // no more tiles
+  int row_in_blk;      // first row within ids[0] (blocks larger than a tile)
+  float ref;           // R
+  float alpha;         // R of the tile before / R
+  int item_s, item_g;  // item: sequence, kv head
+  int part, nparts;    // this item's part of the (sequence, kv head)
+  int group0;          // group holding part 0
+  int slot0;           // partial slot (0 or 1) of part 0 in its CTA
+  int which;           // this part's slot
+  int pad[2];
+};
+static_assert(sizeof(TileRec) == 256, "tile record");
+
+// what the epilogue needs of an item
+struct ItemRec {
+  int s, g, part, nparts, group0, slot0, which, stop;
+};
+static_assert(sizeof(ItemRec) == 32, "item record");
+
+template <int G>
+struct Cfg {
+  static constexpr int NSR = round_up(3 * G, 16);   // rows of q terms (the MMA's N)
+  static constexpr int NPR = round_up(2 * G, 16);   // rows of P terms
+  static constexpr int NP = G > 8 ? 2 : 3;          // P buffers
+  static constexpr int NS = 4;                      // S buffers in tensor memory
+  static constexpr int kQBytes = NSR * 128;
+  static constexpr int kPChunk = NPR * 128;         // P terms of 128 positions
+  static constexpr int kPBytes = 2 * kPChunk;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = NK * kTileBytes;
+  static constexpr int kOffQ = kOffV + NV * kTileBytes;
+  static constexpr int kOffP = kOffQ + QN * kQBytes;
+  static constexpr int kOffRec = kOffP + NP * kPBytes;
+  static constexpr int kOffRed = kOffRec + ND * static_cast<int>(sizeof(TileRec));
+  // [2][G][8] maxima, [8][G] sums
+  static constexpr int kOffQs = round_up(kOffRed + 3 * 8 * G * 4, 16);
+  static constexpr int kEpiBytes = 32 + 36 * 4;  // item record, m and l per head, R
+  static constexpr int kOffEpi = round_up(kOffQs + QN * G * 4, 16);
+  static constexpr int kOffBar = round_up(kOffEpi + NO * kEpiBytes, 16);
+  static constexpr int kNumBars = 3 * ND + 2 * NK + 2 * NV + 2 * NS + 2 * NP + 2 * QN + 4 * NO + 1;
+  static constexpr int kOffMisc = round_up(kOffBar + 8 * kNumBars, 16);
+  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
+  static constexpr uint32_t kSCols = 2 * NSR;  // two products of 128 positions
+  static constexpr uint32_t kTmemO = NS * kSCols;
+  static constexpr uint32_t kTmemUsed = kTmemO + NO * NPR;
+  static constexpr uint32_t kTmemCols = kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kTmemUsed <= 512, "tensor memory");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kQBytes % 1024 == 0 && kPChunk % 1024 == 0,
+                "swizzled operands");
+  static_assert(kOffRec % 16 == 0 && kOffBar % 8 == 0 && kOffEpi % 16 == 0, "alignment");
+  static_assert(NP <= NV, "the softmax's wait for a V tile relies on it (see the top)");
+};
+
+struct BsParams {
+  __nv_bfloat16* out;
+  const __nv_bfloat16* q;
+  const float* k_scales;  // [num_blocks, Hkv]
+  const float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  unsigned long long* counters;  // [2 * grid] first merge level, [2 * grid] second
+  float* ws_o;                   // [4 * grid][G][128]: partials, then the first level's results
+  float* ws_ml;                  // [4 * grid][G][2]
+  unsigned* err;
+  unsigned long long tag;
+  unsigned long long wait_ns;
+  int num_seqs;
+  int num_kv_heads;
+  int members;  // CTAs of a group
+  int groups;
+  int max_blocks;
+  int num_blocks;
+  int bs_log2;
+  int max_context_len;
+  float scale_log2;
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// The first 3 G (scores) or 2 G (outputs) fp32 columns at taddr, rounded up to a load's size.
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float (&v)[N]) {
+  static_assert(N == 2 || N == 4 || N == 8 || N == 16 || N == 32 || N == 48, "columns");
+  if constexpr (N <= 16) {
+    tmem_ld_cols<N>(taddr, v);
+  } else {
+    float t[32];
+    tmem_ld32(taddr, t);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = t[i];
+    if constexpr (N == 48) {
+      float u[16];
+      tmem_ld16(taddr + 32, u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[32 + i] = u[i];
+    }
+  }
+}
+constexpr int load_cols(int n) { return n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 48; }
+
+template <int N>
+__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float (&v)[N]) {
+  if constexpr (N == 16) tmem_st16(taddr, v);
+  else tmem_st32(taddr, v);
+}
+
+// One merge step over `cnt` parts: part i's record is at slot_of(i). Thread dl owns output
+// dim dl; l and the unnormalised sums are combined under the largest maximum. Reads bypass
+// L1 (the parts were written by other SMs).
+template <int G, class SlotOf, class Put>
+__device__ __forceinline__ void merge_parts(const BsParams& p, int cnt, int dl, SlotOf slot_of,
+                                            Put put) {
+  constexpr int CH = G <= 2 ? 8 : G <= 4 ? 4 : 2;  // parts in flight per head
+  float M[G], L[G], A[G];
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    M[h] = -INFINITY;
+    L[h] = 0.f;
+    A[h] = 0.f;
+  }
+#pragma unroll 1
+  for (int c0 = 0; c0 < cnt; c0 += CH) {
+    float2 ml[CH][G];
+    float o[CH][G];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const bool in = c0 + i < cnt;
+      const int64_t slot = slot_of(in ? c0 + i : 0);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        ml[i][h] = in ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot * G + h)
+                      : make_float2(-INFINITY, 0.f);
+        o[i][h] = in ? __ldcg(p.ws_o + (slot * G + h) * HD + dl) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      float mc = M[h];
+#pragma unroll
+      for (int i = 0; i < CH; ++i) mc = fmaxf(mc, ml[i][h].x);
+      const float r = ex2_approx(M[h] - mc);  // 0 for the first chunk; every part has a finite max
+      L[h] *= r;
+      A[h] *= r;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const float f = ex2_approx(ml[i][h].x - mc);
+        L[h] += ml[i][h].y * f;
+        A[h] += o[i][h] * f;
+      }
+      M[h] = mc;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < G; ++h) put(h, M[h], L[h], A[h]);
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_blockscale_kernel(const __grid_constant__ CUtensorMap tmK,
+                             const __grid_constant__ CUtensorMap tmV,
+                             const __grid_constant__ CUtensorMap tmKt,
+                             const __grid_constant__ CUtensorMap tmVt, const BsParams p) {
+  using C = Cfg<G>;
+  constexpr int NS = C::NS, NP = C::NP, NSR = C::NSR, NPR = C::NPR;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int Hq = p.num_kv_heads * G;
+  const int bs = 1 << p.bs_log2;
+  const unsigned long long wl = p.wait_ns;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* rec_full = bars;            // [ND] block ids of a tile -> producer, issuer, softmax
+  uint64_t* scl_full = rec_full + ND;   // [ND] its scales -> softmax
+  uint64_t* rec_empty = scl_full + ND;  // [ND] producer, issuer and softmax are done with it
+  uint64_t* k_full = rec_empty + ND;    // [NK] TMA -> issuer
+  uint64_t* k_empty = k_full + NK;      // [NK] score product done -> producer
+  uint64_t* v_full = k_empty + NK;      // [NV] TMA -> issuer (+ softmax on a last tile)
+  uint64_t* v_empty = v_full + NV;      // [NV] value product done -> producer
+  uint64_t* s_full = v_empty + NV;      // [NS] score product done -> softmax
+  uint64_t* s_free = s_full + NS;       // [NS] softmax has read S
+  uint64_t* p_full = s_free + NS;       // [NP] P written -> issuer
+  uint64_t* pv_done = p_full + NP;      // [NP] value product done -> softmax
+  uint64_t* q_ready = pv_done + NP;     // [QN] q terms and scales written
+  uint64_t* q_empty = q_ready + QN;     // [QN] score products of the item done, scales read
+  uint64_t* o_full = q_empty + QN;      // [NO] item's value products done -> epilogue
+  uint64_t* o_free = o_full + NO;       // [NO] epilogue has read O
+  uint64_t* epi_full = o_free + NO;     // [NO] softmax hand-off
+  uint64_t* epi_empty = epi_full + NO;  // [NO] epilogue has read it
+  uint64_t* mma_drain = epi_empty + NO;
+  TileRec* recs = reinterpret_cast<TileRec*>(smem + C::kOffRec);
+  float* red = reinterpret_cast<float*>(smem + C::kOffRed);
+  float* qscale = reinterpret_cast<float*>(smem + C::kOffQs);  // [QN][G]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
+
+  const int member = blockIdx.x % p.members;
+  const int group = blockIdx.x / p.members;
+  const int hgroups = p.num_kv_heads / p.members;
+
+  // The scheduler warp counts the tiles and finds its run before the set-up barrier, so
+  // that the context lengths' latency overlaps the set-up.
+  unsigned long long units = 0, u0 = 0, u1 = 0;
+  int groups = 1;
+  auto tiles_of = [&](int s) -> int {
+    if (s >= p.num_seqs) return 0;
+    int ctx = __ldg(p.context_lens + s);
+    ctx = ctx > p.max_context_len ? p.max_context_len : ctx;
+    return ctx > 0 ? (ctx + TT - 1) / TT : 0;
+  };
+  if (warp == 14) {
+    unsigned long long sum = 0;
+#pragma unroll 4
+    for (int s = lane; s < p.num_seqs; s += 32) sum += tiles_of(s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    units = sum * hgroups;
+    groups = units < static_cast<unsigned long long>(p.groups) ? static_cast<int>(units) : p.groups;
+    if (group < groups) {
+      u0 = units * group / groups;
+      u1 = units * (group + 1) / groups;
+    }
+  }
+
+  // q slots and P buffers start at zero: rows that no head uses stay zero
+  for (int i = tid; i < (QN * C::kQBytes + NP * C::kPBytes) / 16; i += kThreads)
+    reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  if (tid == 0) {
+    for (int i = 0; i < ND; ++i) {
+      mbar_init(&rec_full[i], 1);
+      mbar_init(&scl_full[i], 1);
+      mbar_init(&rec_empty[i], 2 + kSoftThreads / 32);
+    }
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], kSoftThreads / 32);
+    }
+    for (int i = 0; i < NP; ++i) {
+      mbar_init(&p_full[i], kSoftThreads / 32);
+      mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < QN; ++i) {
+      mbar_init(&q_ready[i], 1);
+      mbar_init(&q_empty[i], 2);
+    }
+    for (int i = 0; i < NO; ++i) {
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+      mbar_init(&epi_full[i], 1);
+      mbar_init(&epi_empty[i], 1);
+    }
+    mbar_init(mma_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 12) {
+    // ======================================================== TMA producer
+    if (lane == 0) {
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+    }
+    __syncwarp();
+    const int rows = bs < TT ? bs : TT;    // rows per box of a full tile
+    const int trows = bs < 32 ? bs : 32;   // of a context's last tile (no rows past it)
+    unsigned jk = 0, jv = 0;  // K and V tiles whose loads were started
+    while (true) {
+      const int rs = jk % ND;
+      if (!warp_wait_or_abort(&rec_full[rs], (jk / ND) & 1, p.err, abort_flag, wl)) break;
+      const TileRec& rec = recs[rs];
+      if (rec.stop) break;
+      const bool full = rec.n == TT;
+      const int br = full ? rows : trows;
+      const int nbox = (rec.n + br - 1) / br;
+      const int bytes = nbox * br * HD;
+      auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar) {
+        mbar_arrive_expect_tx_w(bar, bytes);
+#pragma unroll 1
+        for (int b = 0; b < nbox; ++b) {
+          const int r = b * br + rec.row_in_blk;  // row counted from the first block's start
+          const int row = (rec.ids[r >> p.bs_log2] << p.bs_log2) + (r & (bs - 1));
+          tma_load_3d_w(dst + b * br * HD, map, bar, 0, rec.item_g, row);
+        }
+      };
+      const int ks = jk % NK, vs = jv % NV;
+      if (jk >= NK && !warp_wait_or_abort(&k_empty[ks], ((jk / NK) - 1) & 1, p.err, abort_flag, wl))
+        break;
+      load(full ? &tmK : &tmKt, smem + C::kOffK + ks * kTileBytes, &k_full[ks]);
+      ++jk;
+      if (jv >= NV && !warp_wait_or_abort(&v_empty[vs], ((jv / NV) - 1) & 1, p.err, abort_flag, wl))
+        break;
+      load(full ? &tmV : &tmVt, smem + C::kOffV + vs * kTileBytes, &v_full[vs]);
+      ++jv;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rec_empty[rs]);
+    }
+    // Every copy this warp started must have landed before the CTA ends; per slot only its
+    // last one can still be in flight.
+    if (lane == 0) {
+#pragma unroll 1
+      for (unsigned t = jk > NK ? jk - NK : 0; t < jk; ++t)
+        mbar_wait(&k_full[t % NK], (t / NK) & 1, p.err);
+#pragma unroll 1
+      for (unsigned t = jv > NV ? jv - NV : 0; t < jv; ++t)
+        mbar_wait(&v_full[t % NV], (t / NV) & 1, p.err);
+    }
+  } else if (warp == 14) {
+    // ======================================================== scheduler
+    unsigned j = 0;  // tile records published
+    int k = 0;       // items
+    bool alive = true;
+    // the sequence and head group of unit u0: walk the sequences 32 at a time
+    unsigned long long cum = 0;  // units before sequence s0
+    int s0 = 0;
+    int s = 0, hg = 0, nt = 0;
+    if (u0 < u1) {
+      while (true) {
+        const int t = tiles_of(s0 + lane);
+        int inc = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += up;
+        }
+        const int total = __shfl_sync(0xffffffffu, inc, 31);
+        if (cum + static_cast<unsigned long long>(total) * hgroups > u0) {
+          const unsigned hit = __ballot_sync(
+              0xffffffffu, cum + static_cast<unsigned long long>(inc) * hgroups > u0);
+          const int at = __ffs(hit) - 1;
+          nt = __shfl_sync(0xffffffffu, t, at);
+          const int before = __shfl_sync(0xffffffffu, inc - t, at);
+          cum += static_cast<unsigned long long>(before) * hgroups;
+          s = s0 + at;
+          break;
+        }
+        cum += static_cast<unsigned long long>(total) * hgroups;
+        s0 += 32;
+      }
+      hg = static_cast<int>((u0 - cum) / nt);
+      cum += static_cast<unsigned long long>(hg) * nt;  // units before (s, hg)
+    }
+    unsigned long long u = u0;
+    while (alive && u < u1) {
+      // item: the tiles of (s, hg) inside [u, u1)
+      const int ta = static_cast<int>(u - cum);
+      const unsigned long long end = cum + nt < u1 ? cum + nt : u1;
+      const int tb = static_cast<int>(end - cum);
+      const int g = hg * p.members + member;
+      int ctx = __ldg(p.context_lens + s);
+      if (ctx > p.max_context_len) {
+        if (lane == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+        ctx = p.max_context_len;
+      }
+      // q first: its latency runs under the block ids'
+      uint2 qraw[G];
+      {
+        const uint2* src = reinterpret_cast<const uint2*>(
+            p.q + (static_cast<int64_t>(s) * Hq + g * G) * HD);
+#pragma unroll
+        for (int h = 0; h < G; ++h) qraw[h] = __ldg(src + h * (HD / 4) + lane);
+      }
+      // parts of (s, hg): group i holds units [units i / groups, units (i + 1) / groups)
+      const unsigned long long ng = groups;
+      const int gf = static_cast<int>(((cum + 1) * ng - 1) / units);
+      const int gl = static_cast<int>(((cum + nt) * ng - 1) / units);
+      const int slot0 = units * gf / ng == cum ? 0 : 1;
+      const int part = group - gf;
+      const int which = part == 0 ? slot0 : 0;
+      const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks;
+      const int nblk = (ctx + bs - 1) >> p.bs_log2;
+      const int per_tile = bs >= TT ? 1 : TT >> p.bs_log2;
+      float ref = 0.f;
+      int bb = -32;  // first block of the batch of 32 held by the lanes
+      int id = 0;
+      float ksc = 0.f, vsc = 0.f;
+      for (int t = ta; t < tb; ++t) {
+        const int slot = j % ND;
+        if (j >= ND &&
+            !warp_wait_or_abort(&rec_empty[slot], ((j / ND) - 1) & 1, p.err, abort_flag, wl)) {
+          alive = false;
+          break;
+        }
+        TileRec& rec = recs[slot];
+        const int b0 = static_cast<int>((static_cast<int64_t>(t) * TT) >> p.bs_log2);
+        if (b0 >= bb + 32 || bb < 0) {
+          bb = b0;
+          const int b = bb + lane;
+          id = -1;
+          if (b < nblk && b < p.max_blocks) id = __ldg(table + b);
+          if (id < 0 || id >= p.num_blocks) {
+            if (b < nblk) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+            id = 0;  // in-bounds stand-in
+          }
+        }
+        const int l0 = b0 - bb;
+        const bool mine = lane >= l0 && lane < l0 + per_tile;
+        if (mine) rec.ids[lane - l0] = id;
+        if (lane == 0) {
+          rec.n = ctx - t * TT < TT ? ctx - t * TT : TT;
+          rec.first = t == ta;
+          rec.last = t == tb - 1;
+          rec.stop = 0;
+          rec.row_in_blk = bs > TT ? (t * TT) & (bs - 1) : 0;
+          rec.item_s = s;
+          rec.item_g = g;
+          rec.part = part;
+          rec.nparts = gl - gf + 1;
+          rec.group0 = gf;
+          rec.slot0 = slot0;
+          rec.which = which;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rec_full[slot]);
+        // the scales follow (the tile's loads do not wait for them)
+        if (b0 == bb) {
+          const int64_t at = static_cast<int64_t>(id) * p.num_kv_heads + g;
+          ksc = __ldg(p.k_scales + at);
+          vsc = __ldg(p.v_scales + at);
+        }
+        const bool used = mine && b0 + (lane - l0) < nblk;
+        const float top = warp_max(used ? vsc : 0.f);
+        const float now = fmaxf(ref, top);
+        if (mine) {
+          rec.ks[lane - l0] = ksc;
+          rec.vs[lane - l0] = now > 0.f ? __fdiv_rn(vsc, now) : 0.f;
+        }
+        if (lane == 0) {
+          rec.ref = now;
+          rec.alpha = (t == ta || now == ref || ref == 0.f) ? 1.f : __fdiv_rn(ref, now);
+        }
+        ref = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scl_full[slot]);
+        ++j;
+        if (t == ta) {
+          // q terms of the item: lane L holds dims 4L .. 4L + 3
+          const int qs = k % QN;
+          if (k >= QN &&
+              !warp_wait_or_abort(&q_empty[qs], ((k / QN) - 1) & 1, p.err, abort_flag, wl)) {
+            alive = false;
+            break;
+          }
+          uint8_t* qd = smem + C::kOffQ + qs * C::kQBytes;
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float f0 = bf16lo_to_f32(qraw[h].x), f1 = bf16hi_to_f32(qraw[h].x);
+            const float f2 = bf16lo_to_f32(qraw[h].y), f3 = bf16hi_to_f32(qraw[h].y);
+            const float amax = warp_max(fmaxf(fmaxf(fabsf(f0), fabsf(f1)), fmaxf(fabsf(f2), fabsf(f3))));
+            float inv = 448.f / amax;
+            if (!(inv <= FLT_MAX)) inv = 0.f;  // all zero (or tiny): codes 0, scale 0
+            float y[4] = {f0 * inv, f1 * inv, f2 * inv, f3 * inv};
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+              const int row = 3 * h + term;
+              float2 b01, b23;
+              const uint32_t c01 = e4m3x2(y[0], y[1], b01);
+              const uint32_t c23 = e4m3x2(y[2], y[3], b23);
+              *reinterpret_cast<uint32_t*>(qd + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
+                                           (lane & 3) * 4) = c01 | (c23 << 16);
+              y[0] -= b01.x;
+              y[1] -= b01.y;
+              y[2] -= b23.x;
+              y[3] -= b23.y;
+            }
+            if (lane == 0) qscale[qs * G + h] = inv > 0.f ? amax / 448.f : 0.f;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_ready[qs]);
+        }
+      }
+      ++k;
+      u = end;
+      // next (s, hg)
+      cum = cum + nt;
+      if (u < u1 && ++hg == hgroups) {
+        hg = 0;
+        do {
+          ++s;
+          nt = tiles_of(s);
+        } while (nt == 0 && s < p.num_seqs);
+      }
+    }
+    if (alive) {
+      const int slot = j % ND;
+      if (j < ND ||
+          warp_wait_or_abort(&rec_empty[slot], ((j / ND) - 1) & 1, p.err, abort_flag, wl)) {
+        if (lane == 0) {
+          recs[slot].stop = 1;
+          recs[slot].first = recs[slot].last = recs[slot].n = 0;
+          mbar_arrive(&rec_full[slot]);
+        }
+      }
+    }
+  } else if (warp == 13) {
+    // ======================================================== tensor-core issuer
+    constexpr uint32_t idS = idesc_e4m3_f32(TM, NSR, 0, 0);  // K K-major, q terms K-major
+    constexpr uint32_t idO = idesc_e4m3_f32(HD, NPR, 1, 0);  // V^T MN-major, P terms K-major
+    const uint32_t sP = smem_u32(smem + C::kOffP);
+    unsigned js = 0, jp = 0;  // score and value cursors (tiles)
+    int ks = 0, kp = 0;       // their items
+    bool s_end = false;
+    // S of tile js (false: its record, q, K tile or S buffer is not ready)
+    auto score = [&]() -> bool {
+      if (s_end) return false;
+      const int rs = js % ND;
+      if (!__all_sync(0xffffffffu, mbar_test_wait(&rec_full[rs], (js / ND) & 1))) return false;
+      const TileRec& rec = recs[rs];
+      if (rec.stop) {
+        s_end = true;
+        return false;
+      }
+      const int kslot = js % NK, sb = js % NS, qs = ks % QN;
+      if (!__all_sync(0xffffffffu,
+                      mbar_test_wait(&k_full[kslot], (js / NK) & 1) &&
+                          (js < NS || mbar_test_wait(&s_free[sb], ((js / NS) - 1) & 1)) &&
+                          (!rec.first || mbar_test_wait(&q_ready[qs], (ks / QN) & 1))))
+        return false;
+      tc_fence_after();
+      const uint64_t aK = smem_desc_sw128(smem_u32(smem + C::kOffK + kslot * kTileBytes), 16, 1024);
+      const uint64_t bQ = smem_desc_sw128(smem_u32(smem + C::kOffQ + qs * C::kQBytes), 16, 1024);
+      const uint32_t dS = tmem + sb * C::kSCols;
+#pragma unroll
+      for (int kk = 0; kk < HD / 32; ++kk)
+        tc_mma_f8_ss(dS, desc_advance(aK, kk * 32), desc_advance(bQ, kk * 32), idS, kk > 0 ? 1u : 0u);
+      if (rec.n > TM) {
+#pragma unroll
+        for (int kk = 0; kk < HD / 32; ++kk)
+          tc_mma_f8_ss(dS + NSR, desc_advance(aK, kHalf + kk * 32), desc_advance(bQ, kk * 32), idS,
+                       kk > 0 ? 1u : 0u);
+      }
+      tc_commit(&s_full[sb]);
+      tc_commit(&k_empty[kslot]);
+      if (rec.last) {
+        tc_commit(&q_empty[qs]);
+        ++ks;
+      }
+      ++js;
+      return true;
+    };
+    // O += V^T P^T of tile jp (false: P, V or the accumulator is not ready)
+    auto value = [&]() -> bool {
+      const int pb = jp % NP, vs = jp % NV, ob = kp % NO;
+      const TileRec& rec = recs[jp % ND];
+      const bool first = rec.first != 0;
+      if (!__all_sync(0xffffffffu,
+                      mbar_test_wait(&p_full[pb], (jp / NP) & 1) &&
+                          mbar_test_wait(&v_full[vs], (jp / NV) & 1) &&
+                          (!first || kp < NO || mbar_test_wait(&o_free[ob], ((kp / NO) - 1) & 1))))
+        return false;
+      tc_fence_after();
+      const uint64_t aV = smem_desc_sw128(smem_u32(smem + C::kOffV + vs * kTileBytes), kHalf, 1024);
+      const uint64_t bP = smem_desc_sw128(sP + pb * C::kPBytes, 16, 1024);
+      const uint32_t dO = tmem + C::kTmemO + ob * NPR;
+      const int steps = (rec.n + 31) >> 5;  // 32 positions each; none past the context
+#pragma unroll
+      for (int kk = 0; kk < TT / 32; ++kk)
+        if (kk < steps)
+          tc_mma_f8_ss(dO, desc_advance(aV, kk * 32 * 128),
+                       desc_advance(bP, (kk >> 2) * C::kPChunk + (kk & 3) * 32), idO,
+                       (first && kk == 0) ? 0u : 1u);
+      tc_commit(&pv_done[pb]);
+      tc_commit(&v_empty[vs]);
+      if (rec.last) {
+        tc_commit(&o_full[ob]);
+        ++kp;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rec_empty[jp % ND]);
+      ++jp;
+      return true;
+    };
+    unsigned long long idle_since = 0;
+    while (true) {
+      // a value product first: the softmax and the V ring wait on it
+      const bool progressed = (jp < js && value()) || (js < jp + NS && score());
+      if (jp == js && s_end) break;
+      if (progressed) {
+        idle_since = 0;
+        continue;
+      }
+      if (jp < js)
+        mbar_try_wait(&p_full[jp % NP], (jp / NP) & 1);
+      else
+        mbar_try_wait(&k_full[js % NK], (js / NK) & 1);
+      const unsigned long long now = globaltimer_ns();
+      if (idle_since == 0) idle_since = now;
+      const bool give_up = *abort_flag || now - idle_since > wl;
+      if (__any_sync(0xffffffffu, give_up)) {
+        if (!*abort_flag) {
+          if (lane == 0) flag_error(p.err, PA_DEV_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        break;
+      }
+    }
+    // every product has finished before tensor and shared memory go away
+    tc_commit(mma_drain);
+    mbar_wait(mma_drain, 0, p.err);
+  } else if (warp < 8) {
+    // ======================================================== softmax
+    // Thread r of group sg owns position 128 sg + r of each tile. Control flow is uniform
+    // over the 256 threads: a failed wait only marks `failed`, and the barrier that every
+    // tile has (the exchange of maxima) votes on it before anything of the tile's record
+    // decides a branch around a barrier.
+    const int sg = warp >> 2;
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const int pos = sg * TM + r;  // within the tile
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const int blk = bs >= TT ? 0 : pos >> p.bs_log2;  // block of the tile
+    constexpr int SC = load_cols(3 * G);
+    unsigned j = 0;
+    int k = 0;
+    float m[G], l[G], fs[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      m[h] = 0.f;
+      l[h] = 0.f;
+      fs[h] = 0.f;
+    }
+    bool failed = false;
+    while (true) {
+      const int rs = j % ND, sb = j % NS;
+      failed |= !wait_or_abort(&rec_full[rs], (j / ND) & 1, p.err, abort_flag, wl);
+      const TileRec& rec = recs[rs];
+      const bool stop = rec.stop != 0;
+      float x[G];
+      bool valid = false, first = false;
+      float vrel = 0.f;
+      float* rb = red + (j & 1) * 8 * G;
+      // warp-uniform: the loads below are warp-wide
+      if (__all_sync(0xffffffffu, !failed && !stop)) {
+        first = rec.first != 0;
+        valid = pos < rec.n;
+        failed |= !wait_or_abort(&scl_full[rs], (j / ND) & 1, p.err, abort_flag, wl);
+        if (first) {
+          const int qs = k % QN;
+          failed |= !wait_or_abort(&q_ready[qs], (k / QN) & 1, p.err, abort_flag, wl);
+#pragma unroll
+          for (int h = 0; h < G; ++h) fs[h] = p.scale_log2 * qscale[qs * G + h];
+        }
+        const float ksc = rec.ks[blk];
+        vrel = valid ? rec.vs[blk] : 0.f;
+        failed |= !wait_or_abort(&s_full[sb], (j / NS) & 1, p.err, abort_flag, wl);
+        tc_fence_after();
+        float sv[SC];
+        tmem_ld_n<SC>(tmem + sb * C::kSCols + sg * NSR + lane_off, sv);
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[sb]);
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float d = (sv[3 * h] + sv[3 * h + 1]) + sv[3 * h + 2];
+          x[h] = valid ? d * (fs[h] * ksc) : -INFINITY;
+          const float v = warp_max(x[h]);
+          if (lane == 0) rb[h * 8 + warp] = v;
+        }
+      }
+      if (bar_or(1, kSoftThreads, failed || stop)) {
+        if (tid == 0 && stop && !failed) {  // tell the epilogue there are no more items
+          const int b = k % NO;
+          if (k < NO || wait_or_abort(&epi_empty[b], ((k / NO) - 1) & 1, p.err, abort_flag, wl)) {
+            reinterpret_cast<ItemRec*>(smem + C::kOffEpi + b * C::kEpiBytes)->stop = 1;
+            mbar_arrive(&epi_full[b]);
+          }
+        }
+        break;
+      }
+      // from here the record is known to be sound for every thread
+      if (first && tid == 0) mbar_arrive(&q_empty[k % QN]);  // every thread has its q scales
+      const int n = rec.n;
+      const bool last = rec.last != 0;
+      const float av = rec.alpha;
+      bool rescale = av != 1.f;
+      float alpha[G], pp[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float4 w0 = *reinterpret_cast<const float4*>(rb + h * 8);
+        const float4 w1 = *reinterpret_cast<const float4*>(rb + h * 8 + 4);
+        const float mx = fmaxf(fmax3(fmaxf(w0.x, w0.y), w0.z, w0.w),
+                               fmax3(fmaxf(w1.x, w1.y), w1.z, w1.w));
+        alpha[h] = av;
+        if (first) {
+          m[h] = mx - kTarget;
+          l[h] = 0.f;
+        } else if (mx > m[h] + kBound) {
+          const float mn = mx - kTarget;
+          const float f = ex2_approx(m[h] - mn);
+          alpha[h] *= f;
+          l[h] *= f;
+          m[h] = mn;
+          rescale = true;
+        }
+        const float e = valid ? ex2_approx(x[h] - m[h]) : 0.f;
+        l[h] += e;
+        pp[h] = e * vrel;
+      }
+      if (first) rescale = false;  // O is overwritten by the item's first product
+      // this P buffer was last read by the value product of tile j - NP
+      const int pb = j % NP;
+      if (j >= NP)
+        failed |= !wait_or_abort(&pv_done[pb], ((j / NP) - 1) & 1, p.err, abort_flag, wl);
+      {
+        uint8_t* pt = smem + C::kOffP + pb * C::kPBytes + sg * C::kPChunk + (r & 15);
+        const int c = r >> 4;
+#pragma unroll
+        for (int h = 0; h < G; h += 2) {
+          uint32_t hi, lo;
+          split_e4m3x2(pp[h], h + 1 < G ? pp[h + 1] : 0.f, kLoScale, hi, lo);
+#pragma unroll
+          for (int e = 0; e < 2 && h + e < G; ++e) {
+            const int row = 2 * (h + e);
+            pt[row * 128 + (((c ^ row) & 7) << 4)] = static_cast<uint8_t>(hi >> (8 * e));
+            pt[(row + 1) * 128 + (((c ^ (row + 1)) & 7) << 4)] = static_cast<uint8_t>(lo >> (8 * e));
+          }
+        }
+      }
+      if (n < TT) {
+        // rows past the context may hold anything, and 0 * NaN is NaN: clear those that the
+        // value product's steps of 32 positions read
+        if (!valid && pos < ((n + 31) & ~31)) {
+          const int vs = j % NV;
+          failed |= !wait_or_abort(&v_full[vs], (j / NV) & 1, p.err, abort_flag, wl);
+          uint8_t* v = smem + C::kOffV + vs * kTileBytes + pos * HD;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (sg == 0 && rescale) {
+        // uniform over the group; O holds the products up to tile j - 1
+        const unsigned t = j - 1;
+        failed |= !wait_or_abort(&pv_done[t % NP], (t / NP) & 1, p.err, abort_flag, wl);
+        tc_fence_after();
+        constexpr int OC = NPR;  // 16 or 32 columns, 2 per head
+        float o[OC];
+        const uint32_t at = tmem + C::kTmemO + (k % NO) * NPR + lane_off;
+        tmem_ld_n<OC>(at, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          o[2 * h] *= alpha[h];
+          o[2 * h + 1] *= alpha[h];
+        }
+        tmem_st_n<OC>(at, o);
+        tc_wait_st();
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      const float ref = rec.ref;
+      const ItemRec it{rec.item_s, rec.item_g, rec.part, rec.nparts, rec.group0, rec.slot0, rec.which, 0};
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&p_full[pb]);
+        mbar_arrive(&rec_empty[rs]);
+      }
+      ++j;
+      if (last) {
+        // hand the item to the epilogue: l over the 256 positions, m, R
+        float* lb = red + 2 * 8 * G;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          float v = l[h];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == 0) lb[warp * G + h] = v;
+        }
+        named_bar_sync(1, kSoftThreads);
+        if (tid == 0) {
+          const int b = k % NO;
+          if (k >= NO)
+            failed |= !wait_or_abort(&epi_empty[b], ((k / NO) - 1) & 1, p.err, abort_flag, wl);
+          if (!failed) {
+            uint8_t* es = smem + C::kOffEpi + b * C::kEpiBytes;
+            *reinterpret_cast<ItemRec*>(es) = it;
+            float* em = reinterpret_cast<float*>(es + 32);
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+              float L = 0.f;
+#pragma unroll
+              for (int w = 0; w < 8; ++w) L += lb[w * G + h];
+              em[h] = m[h];
+              em[16 + h] = L;
+            }
+            em[32] = ref;
+            mbar_arrive(&epi_full[b]);
+          }
+        }
+        ++k;
+      }
+    }
+  } else {
+    // ======================================================== epilogue (warps 8-11)
+    const int dl = ((warp & 3) << 5) | lane;  // output dim = tensor-memory lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const bool leader = tid == 8 * 32;
+    // this CTA's four counters, tagged ahead of the arrivals
+    if (dl < 4) {
+      unsigned long long* ctr = p.counters + 2 * (blockIdx.x + (dl >> 1) * gridDim.x) + (dl & 1);
+      tagged_install(ctr, *reinterpret_cast<volatile unsigned long long*>(ctr), p.tag, p.err);
+    }
+    // empty contexts: a zero row for every head
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
+      if (__ldg(p.context_lens + s) <= 0)
+        for (int i = dl; i < Hq * HD / 2; i += 128)
+          reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(s) * Hq * HD)[i] = 0u;
+    int k = 0;
+    while (true) {
+      const int b = k % NO;
+      bool failed = !wait_or_abort(&epi_full[b], (k / NO) & 1, p.err, abort_flag, wl);
+      const uint8_t* es = smem + C::kOffEpi + b * C::kEpiBytes;
+      const ItemRec it = *reinterpret_cast<const ItemRec*>(es);
+      float m[G], L[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        m[h] = reinterpret_cast<const float*>(es + 32)[h];
+        L[h] = reinterpret_cast<const float*>(es + 32)[16 + h];
+      }
+      const float ref = reinterpret_cast<const float*>(es + 32)[32];
+      if (bar_or(2, 128, failed)) break;  // every thread has read the hand-off
+      if (leader) mbar_arrive(&epi_empty[b]);
+      if (it.stop) break;
+      failed |= !wait_or_abort(&o_full[b], (k / NO) & 1, p.err, abort_flag, wl);
+      tc_fence_after();
+      constexpr int OC = load_cols(2 * G);
+      float oc[OC], o[G];
+      tmem_ld_n<OC>(tmem + C::kTmemO + b * NPR + lane_off, oc);
+      tc_wait_ld();
+#pragma unroll
+      for (int h = 0; h < G; ++h) o[h] = fmaf(oc[2 * h + 1], 1.f / kLoScale, oc[2 * h]) * ref;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[b]);
+      const int64_t row0 = static_cast<int64_t>(it.s) * Hq + it.g * G;
+      if (it.nparts == 1) {
+        if (!failed) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(o[h] / L[h]);
+        }
+      } else {
+        // part i lives in slot 0 of CTA (group0 + i, member), the first one in slot0
+        auto slot_of = [&](int i) -> int64_t {
+          return 2 * (static_cast<int64_t>(it.group0 + i) * p.members + member) + (i == 0 ? it.slot0 : 0);
+        };
+        auto put_partial = [&](int64_t slot, int h, float pm, float pl, float po) {
+          p.ws_o[(slot * G + h) * HD + dl] = po;
+          if (dl == 0) *reinterpret_cast<float2*>(p.ws_ml + (slot * G + h) * 2) = make_float2(pm, pl);
+        };
+        const int64_t second = 2ll * gridDim.x;  // where the first level's results start
+        const int64_t mine = 2ll * blockIdx.x + it.which;
+#pragma unroll
+        for (int h = 0; h < G; ++h) put_partial(mine, h, m[h], L[h], o[h]);
+        auto put_out = [&](int h, float, float pl, float po) {
+          p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(po / pl);
+        };
+        // arrive: written by all 128 threads, one release by the leader
+        auto arrive = [&](unsigned long long* ctr, int total) -> bool {
+          named_bar_sync(2, 128);
+          if (leader) {
+            __threadfence();
+            bool okc = true;
+            const unsigned before = tagged_arrive_many(ctr, p.tag, p.err, &okc);
+            const bool is_last = okc && before == static_cast<unsigned>(total - 1);
+            if (is_last) *reinterpret_cast<volatile unsigned long long*>(ctr) = 0ull;
+            *last_flag = is_last;
+            __threadfence();
+          }
+          named_bar_sync(2, 128);
+          return *last_flag != 0;
+        };
+        const int sub = it.part / kFan, nsub = (it.nparts + kFan - 1) / kFan;
+        const int in_sub = it.nparts - sub * kFan < kFan ? it.nparts - sub * kFan : kFan;
+        bool top = nsub == 1;
+        const bool lead1 = arrive(p.counters + slot_of(sub * kFan), in_sub);
+        if (lead1) {
+          auto at = [&](int i) { return slot_of(sub * kFan + i); };
+          if (top) {
+            merge_parts<G>(p, in_sub, dl, at, put_out);
+          } else {
+            const int64_t to = second + slot_of(sub * kFan);
+            merge_parts<G>(p, in_sub, dl, at,
+                           [&](int h, float pm, float pl, float po) { put_partial(to, h, pm, pl, po); });
+            if (arrive(p.counters + second + slot_of(0), nsub))
+              merge_parts<G>(p, nsub, dl, [&](int i) { return second + slot_of(i * kFan); }, put_out);
+          }
+        }
+      }
+      if (bar_or(2, 128, failed)) break;  // also orders last_flag's reuse
+      ++k;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// CTAs of a group: neighbouring kv heads walked side by side.
+int group_members(int num_kv_heads) {
+  return num_kv_heads % 4 == 0 ? 4 : num_kv_heads % 2 == 0 ? 2 : 1;
+}
+
+template <int G>
+cudaError_t launch_g(const DecodeLaunch& a, BsParams p, cudaStream_t stream) {
+  const int bs = a.cache.block_size;
+  const uint64_t slots = static_cast<uint64_t>(a.cache.num_blocks) * bs;
+  const uint64_t dims[3] = {HD, static_cast<uint64_t>(a.cache.num_kv_heads), slots};
+  const uint32_t box[3] = {HD, 1, static_cast<uint32_t>(bs < TT ? bs : TT)};
+  const uint32_t tail[3] = {HD, 1, static_cast<uint32_t>(bs < 32 ? bs : 32)};
+  CUtensorMap tmK, tmV, tmKt, tmVt;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!encode_tensor_map(&tmK, a.k_cache, u8, 1, 3, dims, box, true) ||
+      !encode_tensor_map(&tmV, a.v_cache, u8, 1, 3, dims, box, true) ||
+      !encode_tensor_map(&tmKt, a.k_cache, u8, 1, 3, dims, tail, true) ||
+      !encode_tensor_map(&tmVt, a.v_cache, u8, 1, 3, dims, tail, true))
+    return cudaErrorInvalidValue;
+  constexpr int smem_bytes = Cfg<G>::kSmemBytes;
+  const cudaError_t e = ensure_max_dynamic_smem(
+      reinterpret_cast<const void*>(decode_blockscale_kernel<G>), smem_bytes);
+  if (e != cudaSuccess) return e;
+  decode_blockscale_kernel<G>
+      <<<p.groups * p.members, kThreads, smem_bytes, stream>>>(tmK, tmV, tmKt, tmVt, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_blockscale_workspace(int32_t num_q_heads, int32_t num_kv_heads) {
+  const size_t grid = static_cast<size_t>(sm_count());
+  const size_t g = static_cast<size_t>(num_q_heads / num_kv_heads);
+  return round_up(static_cast<int>(4 * grid * 8), 256) + 4 * grid * g * (HD + 2) * sizeof(float);
+}
+
+cudaError_t launch_decode_blockscale(const DecodeLaunch& a, void* workspace, cudaStream_t stream) {
+  BsParams p;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  p.err = device_error_word();
+  p.tag = next_call_tag();
+  p.wait_ns = wait_limit_ns();
+  p.num_seqs = a.num_seqs;
+  p.num_kv_heads = a.cache.num_kv_heads;
+  p.members = group_members(a.cache.num_kv_heads);
+  // no more groups than there can be tiles of a head group
+  const int64_t tiles = static_cast<int64_t>(a.num_seqs) *
+                        (a.max_context_len > 0 ? (a.max_context_len + TT - 1) / TT : 1) *
+                        (a.cache.num_kv_heads / p.members);
+  p.groups = sm_count() / p.members;
+  if (p.groups < 1) return cudaErrorInvalidValue;
+  if (tiles < p.groups) p.groups = static_cast<int>(tiles);
+  p.max_blocks = a.max_blocks_per_seq;
+  p.num_blocks = a.cache.num_blocks;
+  p.bs_log2 = 31 - __builtin_clz(static_cast<unsigned>(a.cache.block_size));
+  p.max_context_len = a.max_context_len;
+  p.scale_log2 = a.scale * kLog2eF;
+  const int G = a.num_q_heads / a.cache.num_kv_heads;
+  const size_t grid = static_cast<size_t>(p.groups) * p.members;
+  p.counters = static_cast<unsigned long long*>(workspace);
+  p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                    round_up(static_cast<int>(4 * grid * 8), 256));
+  p.ws_ml = p.ws_o + 4 * grid * G * HD;
+  switch (G) {
+    case 1: return launch_g<1>(a, p, stream);
+    case 2: return launch_g<2>(a, p, stream);
+    case 4: return launch_g<4>(a, p, stream);
+    case 8: return launch_g<8>(a, p, stream);
+    case 16: return launch_g<16>(a, p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pa

@@ -81,6 +81,7 @@
 
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
+#include "decode_common.cuh"
 
 namespace pa {
 namespace {
@@ -170,9 +171,6 @@ struct Cfg {
 };
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr unsigned kCountBits = 24;
-constexpr unsigned long long kCountMask = (1ull << kCountBits) - 1;
-
 struct TcParams {
   __nv_bfloat16* out;
   const __nv_bfloat16* q;        // [B, Hq, D] (read by the scheduler for e4m3 pools)
@@ -210,155 +208,6 @@ struct TcParams {
 struct ItemDesc {
   int s, g, p, t0, n, ntiles, nparts, stop;
 };
-
-// Add one to an epoch-tagged counter and return the count before the add; a counter
-// carrying another epoch's tag counts as zero. The tag is installed first (count 0):
-// a thread that reads a stale tag swaps in (tag, 0), and stops as soon as it sees this
-// call's tag, whoever installed it. After that only atomicAdds touch the counter, and
-// they keep the tag, so the common case is one atomicAdd with no retries even with one
-// producer per SM on one address. Bounded number of attempts.
-__device__ __forceinline__ unsigned tagged_fetch_add(unsigned long long* ctr,
-                                                     unsigned long long tag, unsigned* err,
-                                                     bool* ok) {
-  unsigned long long v = *reinterpret_cast<volatile unsigned long long*>(ctr);
-  int it = 0;
-  while ((v >> kCountBits) != tag) {
-    if (++it > 4096) {
-      flag_error(err, PA_DEV_ERR_TIMEOUT);
-      *ok = false;
-      return 0;
-    }
-    const unsigned long long prev = atomicCAS(ctr, v, tag << kCountBits);
-    v = (prev == v) ? (tag << kCountBits) : prev;
-  }
-  const unsigned long long old = atomicAdd(ctr, 1ull);
-  if ((old >> kCountBits) != tag) {  // the count ran into the tag bits
-    flag_error(err, PA_DEV_ERR_TIMEOUT);
-    *ok = false;
-    return 0;
-  }
-  *ok = true;
-  return static_cast<unsigned>(old & kCountMask);
-}
-
-// Same contract as tagged_fetch_add for a counter that only a few threads ever touch
-// (the arrivals of one sequence's partitions): add first, and only if the tag was
-// stale try to restart the count under this call's tag. With so few contenders this
-// is one atomic in the common case. Bounded number of attempts.
-__device__ __forceinline__ unsigned tagged_arrive(unsigned long long* ctr, unsigned long long tag,
-                                                  unsigned* err, bool* ok) {
-  for (int it = 0; it < 4096; ++it) {
-    const unsigned long long old = atomicAdd(ctr, 1ull);
-    if ((old >> kCountBits) == tag) {
-      *ok = true;
-      return static_cast<unsigned>(old & kCountMask);
-    }
-    if (atomicCAS(ctr, old + 1, (tag << kCountBits) | 1ull) == old + 1) {
-      *ok = true;
-      return 0u;
-    }
-  }
-  flag_error(err, PA_DEV_ERR_TIMEOUT);
-  *ok = false;
-  return 0;
-}
-
-// bounded wait that also gives up once another role has given up
-__device__ __forceinline__ void named_bar_sync(int id, int n) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
-// named barrier that also ORs a flag over the participating threads
-__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
-  unsigned r;
-  asm volatile(
-      "{\n\t.reg .pred q, p;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, %2, %3, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-
-// 16 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// N consecutive fp32 columns of this thread's TMEM lane (N = 1, 2, 4, 8 or 16; the
-// score columns a softmax thread needs are the group's G heads).
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N]) {
-  static_assert(N == 1 || N == 2 || N == 4 || N == 8 || N == 16, "tcgen05.ld column count");
-  uint32_t r[16];
-  if constexpr (N == 1) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr) : "memory");
-  } else if constexpr (N == 2) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];"
-                 : "=r"(r[0]), "=r"(r[1]) : "r"(taddr) : "memory");
-  } else if constexpr (N == 4) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr) : "memory");
-  } else if constexpr (N == 8) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-  } else {
-    float t[16];
-    tmem_ld16(taddr, t);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(t[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-      "r"(__float_as_uint(v[15]))
-      : "memory");
-}
-
-
-// Two values -> their e4m3 codes (round to nearest even, saturated to +-448), packed
-// with a in the low byte, and the values those codes stand for.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b, float2& back) {
-  const __nv_fp8x2_storage_t c =
-      __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
-  back = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return static_cast<uint32_t>(c);
-}
-
-// hi / lo e4m3 terms of two values: hi = e4m3(v), lo = e4m3(lo_scale * (v - hi)),
-// as two packed byte pairs (value a in the low byte of each).
-__device__ __forceinline__ void split_e4m3x2(float a, float b, float lo_scale, uint32_t& hi,
-                                             uint32_t& lo) {
-  float2 h, unused;
-  hi = e4m3x2(a, b, h);
-  lo = e4m3x2((a - h.x) * lo_scale, (b - h.y) * lo_scale, unused);
-}
 
 // Softmax groups: for e4m3 with up to 8 heads per kv head, two groups of four warps take
 // the two 128-position halves of a tile side by side (one position per thread, 480
@@ -1431,22 +1280,6 @@ __global__ void __launch_bounds__(kThreadsOf<G, F8>, 1) decode_tc_kernel(
   }
 }
 
-unsigned long long next_tag() {
-  // per-process random start: a workspace left by another process (or by an earlier
-  // call of this one) never carries the current call's tag
-  static std::atomic<unsigned long long> counter{[] {
-    unsigned long long t = static_cast<unsigned long long>(time(nullptr)) * 0x9E3779B97F4A7C15ull;
-    t ^= static_cast<unsigned long long>(clock()) * 0xC2B2AE3D27D4EB4Full;
-    return t;
-  }()};
-  unsigned long long v;
-  do {
-    v = counter.fetch_add(1) & ((1ull << 40) - 1);
-  } while (v == 0);
-  return v;
-}
-
-
 template <int G, bool F8>
 cudaError_t launch_tc_t(const DecodeLaunch& a, const TcParams& p, cudaStream_t stream) {
   const int bs = a.cache.block_size;
@@ -1489,6 +1322,21 @@ cudaError_t launch_tc_t(const DecodeLaunch& a, const TcParams& p, cudaStream_t s
 
 }  // namespace
 
+unsigned long long next_call_tag() {
+  // per-process random start: a workspace left by another process (or by an earlier
+  // call of this one) never carries the current call's tag
+  static std::atomic<unsigned long long> counter{[] {
+    unsigned long long t = static_cast<unsigned long long>(time(nullptr)) * 0x9E3779B97F4A7C15ull;
+    t ^= static_cast<unsigned long long>(clock()) * 0xC2B2AE3D27D4EB4Full;
+    return t;
+  }()};
+  unsigned long long v;
+  do {
+    v = counter.fetch_add(1) & ((1ull << 40) - 1);
+  } while (v == 0);
+  return v;
+}
+
 bool decode_tc_supported(const DecodeLaunch& a) {
   const int G = a.num_q_heads / a.cache.num_kv_heads;
   const bool g_ok = G == 1 || G == 2 || G == 4 || G == 8 || G == 16;
@@ -1510,7 +1358,7 @@ cudaError_t launch_decode_tc(const DecodeLaunch& a, unsigned long long* counters
   p.ws_o = a.ws_o;
   p.ws_ml = a.ws_ml;
   p.err = device_error_word();
-  p.tag = next_tag();
+  p.tag = next_call_tag();
   p.wait_ns = wait_limit_ns();
   p.num_seqs = a.num_seqs;
   p.num_kv_heads = a.cache.num_kv_heads;

@@ -496,6 +496,249 @@ pa_status pa_decode_fp8(void* out, const void* q, const void* k_codes, const voi
 }
 
 namespace {
+// Rows of `heads` heads of head_dim values, `stride` elements apart.
+bool rows_ok(const void* p, int64_t stride, int64_t heads, int32_t head_dim) {
+  return p && aligned16(p) && stride % 8 == 0 && stride >= heads * head_dim;
+}
+
+pa_status check_rope(const pa_rope_desc& r, int32_t head_dim, const int32_t* positions) {
+  if (r.rot_dim < 0 || r.rot_dim % 2 != 0 || r.rot_dim > head_dim) return PA_ERR_INVALID_ARG;
+  if (r.interleaved != 0 && r.interleaved != 1) return PA_ERR_INVALID_ARG;
+  if (!std::isfinite(r.amplitude)) return PA_ERR_INVALID_ARG;
+  if (r.rot_dim > 0 && (!r.inv_freq || !positions)) return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+}  // namespace
+
+pa_status pa_rope_inv_freq(float* inv_freq_out, float* amplitude_out, int32_t rot_dim, double base,
+                           pa_rope_scaling scaling, double factor, double original_context,
+                           double beta_fast, double beta_slow) {
+  if (!inv_freq_out || rot_dim <= 0 || rot_dim % 2 != 0) return PA_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !std::isfinite(base)) return PA_ERR_INVALID_ARG;
+  const bool scaled = scaling != PA_ROPE_PLAIN;
+  if (scaled && (!(factor >= 1.0) || !std::isfinite(factor))) return PA_ERR_INVALID_ARG;
+  const int half = rot_dim / 2;
+  double low = 0.0, high = 1.0, amplitude = 1.0;
+  switch (scaling) {
+    case PA_ROPE_PLAIN:
+    case PA_ROPE_LINEAR:
+      break;
+    case PA_ROPE_BASE:
+      if (rot_dim <= 2) return PA_ERR_INVALID_ARG;
+      base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+      break;
+    case PA_ROPE_RAMP: {
+      if (!(original_context > 0.0) || !std::isfinite(original_context) || !(beta_slow > 0.0) ||
+          !(beta_fast > beta_slow) || !std::isfinite(beta_fast))
+        return PA_ERR_INVALID_ARG;
+      // the (fractional) pair whose angle makes `turns` turns within the original context
+      auto pair_of = [&](double turns) {
+        return half * std::log(original_context / (2.0 * 3.14159265358979323846 * turns)) /
+               std::log(base);
+      };
+      low = pair_of(beta_fast);
+      high = pair_of(beta_slow);
+      amplitude = 1.0 + 0.1 * std::log(factor);
+      break;
+    }
+    default:
+      return PA_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < half; ++i) {
+    double f = std::pow(base, -static_cast<double>(i) / half);
+    if (scaling == PA_ROPE_LINEAR) f /= factor;
+    if (scaling == PA_ROPE_RAMP) {
+      double ramp = (i - low) / (high - low);
+      ramp = ramp < 0.0 ? 0.0 : ramp > 1.0 ? 1.0 : ramp;
+      f = f * (1.0 - ramp) + f / factor * ramp;
+    }
+    inv_freq_out[i] = static_cast<float>(f);
+  }
+  if (amplitude_out) *amplitude_out = static_cast<float>(amplitude);
+  return PA_OK;
+}
+
+pa_status pa_rope(void* out, int64_t out_stride, const void* x, int64_t x_stride,
+                  int32_t num_tokens, int32_t num_heads, int32_t head_dim,
+                  const int32_t* positions, pa_rope_desc rope, void* stream) {
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_heads < 0) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0 || num_heads == 0) return PA_OK;
+  const pa_status st = check_rope(rope, head_dim, positions);
+  if (st != PA_OK) return st;
+  if (!rows_ok(out, out_stride, num_heads, head_dim) || !rows_ok(x, x_stride, num_heads, head_dim))
+    return PA_ERR_INVALID_ARG;
+  RopeStoreLaunch a{};
+  a.q_out = out;
+  a.q = x;
+  a.q_out_stride = out_stride;
+  a.q_stride = x_stride;
+  a.positions = positions;
+  a.rope = rope;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_heads;
+  a.head_dim = head_dim;
+  return finish(launch_rope_store(a, static_cast<cudaStream_t>(stream)), stream);
+}
+
+pa_status pa_rope_store_kvcache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                void* k_cache, void* v_cache, pa_cache_desc cache,
+                                const int32_t* slot_mapping, int32_t num_tokens,
+                                int32_t num_q_heads, const int32_t* positions, pa_rope_desc rope,
+                                void* stream) {
+  pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0 || num_q_heads < 0) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  st = check_rope(rope, cache.head_dim, positions);
+  if (st != PA_OK) return st;
+  if (num_q_heads > 0 && (!rows_ok(q, q_stride, num_q_heads, cache.head_dim) ||
+                          !rows_ok(q_out, q_out_stride, num_q_heads, cache.head_dim)))
+    return PA_ERR_INVALID_ARG;
+  if (!rows_ok(k, k_stride, cache.num_kv_heads, cache.head_dim) ||
+      !rows_ok(v, v_stride, cache.num_kv_heads, cache.head_dim) || !k_cache || !v_cache ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !slot_mapping)
+    return PA_ERR_INVALID_ARG;
+  RopeStoreLaunch a{};
+  a.q_out = q_out;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out_stride = q_out_stride;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.rope = rope;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = cache.num_kv_heads;
+  a.head_dim = cache.head_dim;
+  a.num_slots = static_cast<int64_t>(cache.num_blocks) * cache.block_size;
+  return finish(launch_rope_store(a, static_cast<cudaStream_t>(stream)), stream);
+}
+
+pa_status pa_rope_store_kvcache_fp8_blockscale(
+    void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+    int64_t k_stride, const void* v, int64_t v_stride, void* k_codes, void* v_codes,
+    float* k_scales, float* v_scales, pa_cache_desc cache, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q, const int32_t* context_lens,
+    int32_t num_seqs, int32_t num_tokens, int32_t max_q_len, int32_t num_q_heads,
+    const int32_t* positions, pa_rope_desc rope, void* stream) {
+  pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_tokens < 0 || max_q_len < 0 || num_q_heads < 0 || max_blocks_per_seq <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_tokens == 0 || max_q_len == 0) return PA_OK;
+  st = check_rope(rope, cache.head_dim, positions);
+  if (st != PA_OK) return st;
+  if (rope.rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  if (num_q_heads > 0 && (!rows_ok(q, q_stride, num_q_heads, cache.head_dim) ||
+                          !rows_ok(q_out, q_out_stride, num_q_heads, cache.head_dim)))
+    return PA_ERR_INVALID_ARG;
+  if (!rows_ok(k, k_stride, cache.num_kv_heads, cache.head_dim) ||
+      !rows_ok(v, v_stride, cache.num_kv_heads, cache.head_dim))
+    return PA_ERR_INVALID_ARG;
+  if (!k_codes || !v_codes || !k_scales || !v_scales || !block_tables || !cu_seqlens_q ||
+      !context_lens || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scales) ||
+      !aligned16(v_scales))
+    return PA_ERR_INVALID_ARG;
+  AppendLaunch a{};
+  a.q_out = q_out;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out_stride = q_out_stride;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.k_codes = k_codes;
+  a.v_codes = v_codes;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.cache = cache;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.cu_seqlens = cu_seqlens_q;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.max_new = max_q_len;
+  a.num_q_heads = num_q_heads;
+  a.positions = positions;
+  a.rope = rope;
+  return finish(launch_append_blockscale(a, static_cast<cudaStream_t>(stream)), stream);
+}
+
+pa_status pa_store_kvcache_fp8_blockscale(const void* k, int64_t k_stride, const void* v,
+                                          int64_t v_stride, void* k_codes, void* v_codes,
+                                          float* k_scales, float* v_scales, pa_cache_desc cache,
+                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* cu_seqlens_q, const int32_t* context_lens,
+                                          int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
+                                          void* stream) {
+  const pa_rope_desc none{nullptr, 0, 0, 1.f};
+  return pa_rope_store_kvcache_fp8_blockscale(
+      nullptr, 0, nullptr, 0, k, k_stride, v, v_stride, k_codes, v_codes, k_scales, v_scales, cache,
+      block_tables, max_blocks_per_seq, cu_seqlens_q, context_lens, num_seqs, num_tokens, max_q_len,
+      0, nullptr, none, stream);
+}
+
+size_t pa_decode_fp8_blockscale_workspace_size(int32_t num_q_heads, int32_t num_kv_heads) {
+  if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0) return 0;
+  return decode_blockscale_workspace(num_q_heads, num_kv_heads);
+}
+
+pa_status pa_decode_fp8_blockscale(void* out, const void* q, const void* k_codes,
+                                   const void* v_codes, const float* k_scales,
+                                   const float* v_scales, pa_cache_desc cache,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, int32_t num_seqs,
+                                   int32_t num_q_heads, float scale, int32_t max_context_len,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  const pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads % cache.num_kv_heads || !std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_context_len) >
+      static_cast<int64_t>(max_blocks_per_seq) * cache.block_size)
+    return PA_ERR_INVALID_ARG;
+  const int G = num_q_heads / cache.num_kv_heads;
+  if (cache.head_dim != 128 || (G != 1 && G != 2 && G != 4 && G != 8 && G != 16))
+    return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_codes || !v_codes || !k_scales || !v_scales || !block_tables || !context_lens)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) ||
+      !aligned16(k_scales) || !aligned16(v_scales))
+    return PA_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < decode_blockscale_workspace(num_q_heads, cache.num_kv_heads))
+    return PA_ERR_INVALID_ARG;
+  DecodeLaunch a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_codes;
+  a.v_cache = v_codes;
+  a.cache = cache;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.scale = scale;
+  a.max_context_len = max_context_len;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  return finish(launch_decode_blockscale(a, workspace, static_cast<cudaStream_t>(stream)), stream);
+}
+
+namespace {
 pa_status prefill_impl(const StoreRows* store, void* out, const void* q, const void* k_cache,
                        const void* v_cache, pa_cache_desc cache, const int32_t* block_tables,
                        int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,

@@ -24,6 +24,10 @@ unsigned* device_error_word();
 // the full 2 s.
 unsigned long long wait_limit_ns();
 
+// The tag of the next call that uses epoch-tagged counters (1 .. 2^40 - 1): unique within
+// the process, with a random start.
+unsigned long long next_call_tag();
+
 // Number of SMs of the current device (cached).
 int sm_count();
 
@@ -104,6 +108,58 @@ inline size_t decode_counter_bytes(int32_t num_seqs, int32_t num_q_heads) {
   const size_t b = 8 * (1 + static_cast<size_t>(num_seqs) * num_q_heads);
   return (b + 255) / 256 * 256;
 }
+
+// Rotary positions of q and k, the k and v rows scattered into the bf16 pools (rope.cu).
+// num_kv_heads 0: only q is turned.
+struct RopeStoreLaunch {
+  void* q_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_out_stride, q_stride, k_stride, v_stride;  // elements between tokens
+  void* k_cache;
+  void* v_cache;
+  const int32_t* slot_mapping;
+  const int32_t* positions;
+  pa_rope_desc rope;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int64_t num_slots;
+};
+cudaError_t launch_rope_store(const RopeStoreLaunch& a, cudaStream_t stream);
+
+// The same rotation with the rows appended to e4m3 pools with block scales
+// (store_blockscale.cu). num_q_heads 0: no queries; rope.rot_dim 0: nothing is turned.
+struct AppendLaunch {
+  void* q_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_out_stride, q_stride, k_stride, v_stride;
+  void* k_codes;
+  void* v_codes;
+  float* k_scales;
+  float* v_scales;
+  pa_cache_desc cache;
+  const int32_t* block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t* cu_seqlens;
+  const int32_t* context_lens;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t max_new;
+  int32_t num_q_heads;
+  const int32_t* positions;
+  pa_rope_desc rope;
+};
+cudaError_t launch_append_blockscale(const AppendLaunch& a, cudaStream_t stream);
+
+// Decode over e4m3 pools with block scales (decode_blockscale.cu). Reads out, q, the pools
+// and their scales ([num_blocks, Hkv]), tables, lengths, sizes and scale of `a`.
+size_t decode_blockscale_workspace(int32_t num_q_heads, int32_t num_kv_heads);
+cudaError_t launch_decode_blockscale(const DecodeLaunch& a, void* workspace, cudaStream_t stream);
 
 struct PrefillLaunch {
   void* out;

@@ -1,0 +1,371 @@
+"""GPU parity of the e4m3 cache with block scales: append (bit for bit against the oracle) and
+decode (the decode bar, and 2^-7 over the whole tensor: the output's rounding to bf16 is at
+most 2^-8 of a value and the two-term probabilities add at most as much)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_442_b200 as pa
+from oracle import fp8_block
+from tests.gpu_helpers import assert_close, bf16_dev, i32_dev, to_bits, to_f64
+from workloads import f32_to_bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+
+def u8_dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.uint8)).cuda()
+
+
+def f32_dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda()
+
+
+def tables_of(rng, ctx, bs, spare=2):
+    """Shuffled block tables; returns (tables, blocks of the pool)."""
+    need = [-(-max(0, int(c)) // bs) for c in ctx]
+    nb = sum(need) + spare
+    perm = rng.permutation(nb)
+    out = np.full((len(ctx), max(1, max(need))), -1, np.int32)
+    at = 0
+    for s, n in enumerate(need):
+        out[s, :n] = perm[at:at + n]
+        at += n
+    return out, nb
+
+
+# ------------------------------------------------------------------------------ append
+def wild_rows(rng, t, hkv, d):
+    """bf16 rows whose sizes vary by row (scales grow as a block fills), with edges."""
+    x = rng.standard_normal((t, hkv, d)) * np.exp(rng.uniform(-3, 3, (t, hkv, 1)))
+    x = x.astype(np.float32)
+    x[0, 0] = 0.0
+    if t > 8:
+        x[2, 0] = 1e-39                      # bf16 subnormals
+        x[3, 0] = 448.0 * 2.0 ** -3          # exactly at a scale's top
+        x[4, -1] = 3e38
+        x[5, 0, :4] = np.inf
+        x[6, 0, 0] = np.nan
+        x[7, 0] = np.round(rng.standard_normal(d) * 4) / 4
+    return f32_to_bf16_bits(x)
+
+
+def pools_of(rng, nb, bs, hkv, d):
+    codes = rng.integers(0, 256, (nb, bs, hkv, d)).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0x33
+    scales = np.ldexp(1.0, rng.integers(-8, 3, (nb, hkv))).astype(np.float32)
+    return codes, scales
+
+
+def same_codes(got, want):
+    """Equal, where both NaN codes count as one."""
+    g, w = got.copy(), want.copy()
+    g[(g & 0x7F) == 0x7F] = 0x7F
+    w[(w & 0x7F) == 0x7F] = 0x7F
+    return np.array_equal(g, w)
+
+
+@pytest.mark.parametrize("hkv,d,bs,new,old", [
+    (8, 128, 256, [1] * 6, [0, 1, 255, 256, 300, 37]),       # decode steps
+    (2, 64, 16, [1, 1, 1], [0, 15, 16]),
+    (2, 128, 16, [40, 0, 16, 7], [0, 5, 8, 9]),               # blocks of 16, one sequence idle
+    (1, 128, 32, [33, 64, 95], [31, 0, 1]),
+    (3, 128, 64, [61, 130, 1], [3, 63, 64]),
+    (2, 128, 256, [600, 256], [10, 0]),                       # whole blocks in registers
+    (1, 64, 512, [700], [100]),
+    (2, 128, 1024, [1500, 900], [700, 0]),                    # blocks read twice
+])
+def test_append_matches_the_oracle_bit_for_bit(hkv, d, bs, new, old):
+    rng = np.random.default_rng(bs + d + sum(new))
+    ctx = np.array(new) + np.array(old)
+    tables, nb = tables_of(rng, ctx, bs)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    k, v = wild_rows(rng, T, hkv, d), wild_rows(rng, T, hkv, d)[::-1].copy()
+    kc, ks = pools_of(rng, nb, bs, hkv, d)
+    vc, vs = pools_of(rng, nb, bs, hkv, d)
+    want_k = fp8_block.append(kc, ks, k, tables, cu, ctx)
+    want_v = fp8_block.append(vc, vs, v, tables, cu, ctx)
+    dk, dv, dks, dvs = u8_dev(kc), u8_dev(vc), f32_dev(ks), f32_dev(vs)
+    pa.pa_store_kvcache_fp8_blockscale(bf16_dev(k), bf16_dev(v), dk, dv, dks, dvs, i32_dev(tables),
+                                       i32_dev(cu), i32_dev(ctx), max(new))
+    assert np.array_equal(dks.cpu().numpy(), want_k[1]) and np.array_equal(dvs.cpu().numpy(), want_v[1])
+    assert same_codes(dk.cpu().numpy(), want_k[0])
+    assert same_codes(dv.cpu().numpy(), want_v[0])
+
+
+@pytest.mark.parametrize("inter,rot", [(False, 128), (True, 64), (False, 16)])
+@pytest.mark.parametrize("new,bs", [([1, 1, 1], 256), ([70, 3], 64)])
+def test_rope_append_equals_rope_then_append(new, bs, inter, rot):
+    rng = np.random.default_rng(rot + bs)
+    hq, hkv, d = 4, 2, 128
+    ctx = np.array(new) + 13
+    tables, nb = tables_of(rng, ctx, bs)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    qkv = bf16_dev(f32_to_bf16_bits(rng.standard_normal((T, hq + 2 * hkv, d)).astype(np.float32)))
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    pos = i32_dev(rng.integers(0, 2 ** 20, T))
+    f = torch.tensor(pa.pa_rope_inv_freq(rot)[0], dtype=torch.float32, device="cuda")
+    kc, ks = pools_of(rng, nb, bs, hkv, d)
+    vc, vs = pools_of(rng, nb, bs, hkv, d)
+    a = [u8_dev(kc), u8_dev(vc), f32_dev(ks), f32_dev(vs)]
+    b = [t.clone() for t in a]
+    q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device="cuda")
+    rest = (i32_dev(tables), i32_dev(cu), i32_dev(ctx), max(new))
+    pa.pa_rope_store_kvcache_fp8_blockscale(q_out, q, k, v, *a, *rest, pos, f, interleaved=inter, amplitude=1.25)
+    rq, rk = torch.empty_like(q_out), torch.empty((T, hkv, d), dtype=torch.bfloat16, device="cuda")
+    pa.pa_rope(rq, q, pos, f, interleaved=inter, amplitude=1.25)
+    pa.pa_rope(rk, k, pos, f, interleaved=inter, amplitude=1.25)
+    pa.pa_store_kvcache_fp8_blockscale(rk, v, *b, *rest)
+    assert np.array_equal(to_bits(q_out), to_bits(rq))
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+def test_append_bad_lengths_and_blocks_are_reported_and_skipped():
+    rng = np.random.default_rng(2)
+    hkv, d, bs = 2, 128, 16
+    k = bf16_dev(f32_to_bf16_bits(rng.standard_normal((6, hkv, d)).astype(np.float32)))
+    kc, ks = pools_of(rng, 5, bs, hkv, d)
+    good = np.array([[1], [2], [3]], np.int32)
+
+    def run(tables, cu, ctx, m=2):
+        t = [u8_dev(kc), u8_dev(kc), f32_dev(ks), f32_dev(ks)]
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_store_kvcache_fp8_blockscale(k, k, *t, i32_dev(tables), i32_dev(np.array(cu)),
+                                               i32_dev(np.array(ctx)), m)
+        assert e.value.status == 3
+        return t[0].cpu().numpy()
+
+    want = fp8_block.append(kc, ks, to_bits(k), good, [0, 2, 4, 6], [2, 2, 2])[0]
+    for tables, cu, ctx, skipped in (
+            (np.array([[1], [5], [3]], np.int32), [0, 2, 4, 6], [2, 2, 2], 2),     # block past the pool
+            (np.array([[1], [-1], [3]], np.int32), [0, 2, 4, 6], [2, 2, 2], 2),
+            (good, [0, 2, 4, 6], [2, 1, 2], 2),                                     # more new than context
+            (good, [0, 2, 4, 6], [2, 17, 2], 2),                                    # context past the table
+            (good, [0, 2, 4, 7], [2, 2, 3], 3)):                                    # past the tokens
+        got = run(tables, cu, ctx, 3)
+        exp = want.copy()
+        exp[skipped] = kc[skipped]
+        assert np.array_equal(got, exp)
+    got = run(good, [0, 2, 5, 6], [2, 3, 1], 2)                                     # above max_q_len
+    assert np.array_equal(got[2], kc[2]) and np.array_equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------------------ decode
+class Case:
+    """Random codes and scales as pools (every byte of rows past a context is a NaN code)."""
+
+    def __init__(self, ctx, hq, hkv, bs, seed, q_factor=1.0, spread=1.0, widen=0):
+        rng = np.random.default_rng(seed)
+        self.ctx = np.array(ctx, np.int32)
+        self.tables, self.nb = tables_of(rng, np.maximum(self.ctx, 0), bs)
+        if widen:
+            self.tables = np.pad(self.tables, ((0, 0), (0, widen)), constant_values=-1)
+        self.q = f32_to_bf16_bits((q_factor * rng.standard_normal((len(ctx), hq, 128))).astype(np.float32))
+        shape = (self.nb, bs, hkv, 128)
+
+        def pool():
+            c = np.full(shape, 0x7F, np.uint8)
+            s = np.full((self.nb, hkv), np.nan, np.float32)
+            for i, n in enumerate(np.maximum(self.ctx, 0)):
+                for b in range(-(-int(n) // bs)):
+                    rows = min(bs, int(n) - b * bs)
+                    x = rng.standard_normal((rows, hkv, 128))
+                    c[self.tables[i, b], :rows] = fp8_block.encode(np.clip(x * 96, -448, 448))
+                    s[self.tables[i, b]] = np.exp(spread * rng.standard_normal(hkv)) / 96
+            return c, s
+        (self.kc, self.ks), (self.vc, self.vs) = pool(), pool()
+        self.bs, self.hkv, self.scale = bs, hkv, 128 ** -0.5
+
+    def gpu(self, ws=None, max_ctx=None, out=None, stream=None):
+        if not hasattr(self, "dev"):
+            self.dev = (bf16_dev(self.q), u8_dev(self.kc), u8_dev(self.vc), f32_dev(self.ks), f32_dev(self.vs),
+                        i32_dev(self.tables), i32_dev(self.ctx))
+        q = self.dev[0]
+        out = torch.full_like(q, float("nan")) if out is None else out
+        ws = pa.decode_fp8_blockscale_workspace(q.shape[0], q.shape[1], self.hkv) if ws is None else ws
+        pa.pa_decode_fp8_blockscale(out, *self.dev, self.scale, int(max(0, self.ctx.max())) if max_ctx is None else max_ctx,
+                                    ws, stream=stream)
+        return out
+
+    def oracle(self):
+        return fp8_block.decode(self.q, self.kc, self.vc, self.ks, self.vs, self.tables, self.ctx, self.scale)
+
+
+def close(gpu, ref, what=""):
+    c = assert_close(to_f64(gpu), ref, what)
+    assert c["norm_rel"] <= 2.0 ** -7, (what, c)
+
+
+@pytest.mark.parametrize("ctx,hq,hkv,bs", [
+    ([1], 1, 1, 16), ([5, 0, 256, 257, -3, 31], 4, 2, 16), ([512], 8, 8, 32), ([100, 700, 33], 16, 8, 256),
+    ([1000, 1, 2047, 64], 32, 8, 64), ([300, 300], 16, 1, 128), ([700, 129], 32, 2, 16), ([1025, 600], 3, 3, 512),
+    ([2500, 1024], 6, 6, 1024), ([9000], 8, 1, 128), ([0, 0], 4, 2, 64), ([40] * 70, 4, 4, 16),
+    ([20000], 2, 1, 16), ([6001, 17], 16, 4, 256),
+])
+def test_decode_matches_the_oracle(ctx, hq, hkv, bs):
+    c = Case(ctx, hq, hkv, bs, seed=len(ctx) + hq + bs)
+    close(c.gpu(), c.oracle(), f"{ctx[:4]} {hq}/{hkv} {bs}")
+
+
+@pytest.mark.parametrize("g", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("q_factor,spread", [(8.0, 0.3), (0.0, 2.0), (30.0, 1.0)])
+def test_decode_peaked_flat_and_uneven_scales(g, q_factor, spread):
+    c = Case([3000, 517, 60], 2 * g, 2, 64, seed=g, q_factor=q_factor, spread=spread)
+    close(c.gpu(), c.oracle(), f"G {g} q x{q_factor} spread {spread}")
+
+
+def test_decode_one_dominant_value_block():
+    """A block whose V scale is 2^9 above the others, anywhere in the context."""
+    for at in (0, 5, 11):
+        c = Case([3000], 4, 2, 256, seed=at)
+        c.vs[c.tables[0, at]] *= 512.0
+        close(c.gpu(), c.oracle(), f"dominant block {at}")
+
+
+def test_decode_zero_value_scales():
+    c = Case([1500, 700], 4, 2, 64, seed=3)
+    c.vs[c.tables[0, :10]] = 0.0          # the first tiles' values are all zero
+    c.vs[c.tables[1, :11]] = 0.0          # every value of the second sequence
+    out = c.gpu()
+    close(out[:1], c.oracle()[:1])
+    assert not to_f64(out)[1].any()
+
+
+def test_decode_is_deterministic_and_reuses_a_workspace():
+    c = Case([7000, 100, 4100, 0, 900], 8, 4, 64, seed=9)
+    big = Case([300] * 40, 8, 4, 16, seed=10)
+    ws = pa.decode_fp8_blockscale_workspace(5, 8, 4)
+    ws.view(torch.int32).fill_(-1)
+    first, other = c.gpu(ws), big.gpu(ws)
+    for _ in range(20):
+        assert torch.equal(c.gpu(ws).view(torch.int16), first.view(torch.int16))
+        assert torch.equal(big.gpu(ws).view(torch.int16), other.view(torch.int16))
+    close(first, c.oracle())
+
+
+def test_decode_graphs_share_a_workspace():
+    """Two captured calls on one workspace, replayed in turn without clearing it."""
+    a, b = Case([5000, 40], 8, 2, 64, seed=21), Case([900] * 9, 8, 2, 16, seed=22)
+    ws = pa.decode_fp8_blockscale_workspace(9, 8, 2)
+    want = [x.gpu(ws) for x in (a, b)]
+    outs = [torch.empty_like(w) for w in want]
+    pa.pa_set_debug_checks(False)
+    try:
+        graphs = []
+        for x, o in zip((a, b), outs):
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                x.gpu(ws, out=o)
+            torch.cuda.current_stream().wait_stream(side)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                x.gpu(ws, out=o)
+            graphs.append(g)
+        for i in (0, 1, 0, 0, 1, 1, 0):
+            outs[i].zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i].view(torch.int16), want[i].view(torch.int16))
+        del graphs
+    finally:
+        pa.pa_set_debug_checks(True)
+    assert pa.pa_check_device_errors() == 0
+
+
+def test_decode_on_two_streams_with_their_own_workspaces():
+    a, b = Case([4000, 300], 8, 2, 64, seed=31), Case([2000] * 6, 16, 2, 32, seed=32)
+    want = [a.gpu().clone(), b.gpu().clone()]
+    torch.cuda.synchronize()
+    pa.pa_set_debug_checks(False)
+    try:
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        ws = [pa.decode_fp8_blockscale_workspace(8, 8, 2), pa.decode_fp8_blockscale_workspace(8, 16, 2)]
+        outs = [torch.empty_like(w) for w in want]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for x, w, o, st in zip((a, b), ws, outs, streams):
+                x.gpu(w, out=o, stream=st)
+        torch.cuda.synchronize()
+    finally:
+        pa.pa_set_debug_checks(True)
+    for o, w in zip(outs, want):
+        assert torch.equal(o.view(torch.int16), w.view(torch.int16))
+
+
+def test_decode_bad_block_id_and_too_long_a_context_are_reported():
+    c = Case([500, 90], 4, 2, 64, seed=4)
+    ok = c.gpu()
+    c.dev[5][0, 2] = c.nb + 7
+    out = torch.zeros_like(ok)
+    with pytest.raises(pa.PAError) as e:
+        c.gpu(out=out)
+    assert e.value.status == 3
+    assert torch.equal(out[1], ok[1])          # the other sequence is not touched by it
+    d = Case([500, 90], 4, 2, 64, seed=4, widen=3)
+    with pytest.raises(pa.PAError) as e:
+        d.gpu(max_ctx=400, out=out)
+    assert e.value.status == 3
+    d.ctx = np.array([400, 90], np.int32)      # clipped to the host's bound
+    close(out, d.oracle())
+
+
+def test_decode_wait_that_runs_out_is_reported():
+    c = Case([700, 129, 3000, 1], 8, 2, 64, seed=33)
+    ws = pa.decode_fp8_blockscale_workspace(4, 8, 2)
+    pa.pa_set_wait_limit_ns(1)
+    try:
+        with pytest.raises(pa.PAError) as e:
+            c.gpu(ws)
+        assert e.value.status == 5
+    finally:
+        pa.pa_set_wait_limit_ns(0)
+    torch.cuda.synchronize()
+    assert pa.pa_check_device_errors() == 0
+    close(c.gpu(ws), c.oracle(), "after a timeout")
+
+
+# --------------------------------------------------------------------- a run of them together
+@pytest.mark.parametrize("bs,rot,inter", [(64, 128, False), (16, 64, True)])
+def test_prefill_then_decode_steps_over_the_block_scaled_cache(bs, rot, inter):
+    """Chunks, then single tokens: rotate and append, decode from the pools. Every step's
+    output follows the values the oracle's pools hold."""
+    rng = np.random.default_rng(bs)
+    hq, hkv, d, B = 8, 2, 128, 3
+    f_host, _ = pa.pa_rope_inv_freq(rot, scaling="linear", factor=2.0)
+    f = torch.tensor(f_host, dtype=torch.float32, device="cuda")
+    steps = [np.array([150, 37, 1]), np.array([30, 0, 80])] + [np.ones(B, int)] * 4
+    total = sum(steps)
+    tables, nb = tables_of(rng, total, bs)
+    kc, ks = pools_of(rng, nb, bs, hkv, d)
+    vc, vs = pools_of(rng, nb, bs, hkv, d)
+    dev = [u8_dev(kc), u8_dev(vc), f32_dev(ks), f32_dev(vs)]
+    ws = pa.decode_fp8_blockscale_workspace(B, hq, hkv)
+    ctx = np.zeros(B, int)
+    for new in steps:
+        ctx = ctx + new
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        T = int(cu[-1])
+        x = f32_to_bf16_bits((rng.standard_normal((T, hq + 2 * hkv, d)) * np.exp(rng.uniform(-1, 1, (T, 1, 1)))).astype(np.float32))
+        qkv = bf16_dev(x)
+        pos = np.concatenate([np.arange(c - n, c) for c, n in zip(ctx, new)]).astype(np.int32)
+        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device="cuda")
+        k = qkv[:, hq:hq + hkv]
+        pa.pa_rope_store_kvcache_fp8_blockscale(q_out, qkv[:, :hq], k, qkv[:, hq + hkv:], *dev, i32_dev(tables),
+                                                i32_dev(cu), i32_dev(ctx), int(new.max()), i32_dev(pos), f,
+                                                interleaved=inter)
+        rk = torch.empty((T, hkv, d), dtype=torch.bfloat16, device="cuda")
+        pa.pa_rope(rk, k, i32_dev(pos), f, interleaved=inter)
+        kc, ks = fp8_block.append(kc, ks, to_bits(rk), tables, cu, ctx)
+        vc, vs = fp8_block.append(vc, vs, x[:, hq + hkv:], tables, cu, ctx)
+        assert np.array_equal(dev[0].cpu().numpy(), kc) and np.array_equal(dev[1].cpu().numpy(), vc)
+        if (new > 0).all():
+            ends = torch.from_numpy(cu[1:].astype(np.int64) - 1).cuda()
+            q = q_out[ends].contiguous()
+            out = torch.empty_like(q)
+            pa.pa_decode_fp8_blockscale(out, q, *dev, i32_dev(tables), i32_dev(ctx), d ** -0.5, int(ctx.max()), ws)
+            close(out, fp8_block.decode(to_bits(q), kc, vc, ks, vs, tables, ctx, d ** -0.5))
