@@ -3,7 +3,7 @@
 // where in the pre-allocated tensor K/V are written; the rotation comes before it).
 //
 // HBM-bound: every q, k and v value is read once and written once. A CTA takes TB tokens,
-// computes their rot_dim / 2 turns each once into shared memory (64-bit angle reduction),
+// computes their rot_dim / 2 turns each once into shared memory (angles in fixed point),
 // then its threads walk over the tokens' heads, one group of 16 dims per thread and head
 // (two 16-byte loads, two 16-byte stores); a thread keeps its 8 turns in registers across
 // the heads. The first loads are issued before the turns are computed, so the two
@@ -84,7 +84,7 @@ template <int D, int TB, int U>
 __global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeStoreParams p) {
   constexpr int NG = D / 16;                   // groups of 16 dims per head
   constexpr int HL = kThreads / (NG * TB);     // heads walked side by side
-  __shared__ float2 turns[TB][D / 2];
+  __shared__ RopeTable<TB, D / 2> table;
   const int tid = threadIdx.x;
   const int g = tid % NG;
   const int tk = (tid / NG) % TB;
@@ -111,18 +111,10 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeStorePar
   };
   load(hl);
 
-  const int half = p.rope.rot_dim >> 1;
-  for (int i = tid; i < TB * half; i += kThreads) {
-    const int tt = i / half, f = i - tt * half;
-    if (t0 + tt < p.num_tokens)
-      turns[tt][f] = rope_turn(__ldg(p.positions + t0 + tt), __ldg(p.rope.inv_freq + f),
-                               p.rope.amplitude);
-  }
+  table.fill(tid, kThreads, t0, p.num_tokens, p.positions, p.rope);
   __syncthreads();
   const bool in_rot = g < (p.rope.rot_dim >> 4);
-  float2 cs[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = in_rot ? turns[tk][8 * g + i] : make_float2(1.f, 0.f);
+  const RopeTurns cs = table.group(tk, in_rot ? g : 0);
 
   for (int h0 = hl; h0 < heads; h0 += U * HL) {
 #pragma unroll
@@ -171,7 +163,8 @@ __global__ void __launch_bounds__(kThreads) rope_store_any_kernel(const RopeStor
     const __nv_bfloat16 a = src[ia], b = src[ib];
     if (turned) {
       const float2 y = rope_pair(__bfloat162float(a), __bfloat162float(b),
-                                 rope_turn(__ldg(p.positions + t), __ldg(p.rope.inv_freq + f),
+                                 rope_turn(__ldg(p.positions + t),
+                                           rope_rate(__ldg(p.rope.inv_freq + f)),
                                            p.rope.amplitude));
       dst[ia] = __float2bfloat16_rn(y.x);
       dst[ib] = __float2bfloat16_rn(y.y);

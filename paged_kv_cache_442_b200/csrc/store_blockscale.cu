@@ -111,7 +111,8 @@ __device__ __forceinline__ uint4 requantise16(uint4 w, float factor) {
 
 // The queries of kQTokens tokens (as in rope.cu).
 template <int D>
-__device__ __forceinline__ void turn_queries(const AppendParams& p, float2 (*turns)[D / 2]) {
+__device__ __forceinline__ void turn_queries(const AppendParams& p,
+                                             RopeTable<kQTokens, D / 2>& table) {
   constexpr int NG = D / 16;
   constexpr int HL = kThreads / (NG * kQTokens);
   const int tid = threadIdx.x;
@@ -134,18 +135,10 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, float2 (*tur
     }
   };
   load(hl);
-  const int half = p.rope.rot_dim >> 1;
-  for (int i = tid; i < kQTokens * half; i += kThreads) {
-    const int tt = i / half, f = i - tt * half;
-    if (t0 + tt < p.num_tokens)
-      turns[tt][f] = rope_turn(__ldg(p.positions + t0 + tt), __ldg(p.rope.inv_freq + f),
-                               p.rope.amplitude);
-  }
+  table.fill(tid, kThreads, t0, p.num_tokens, p.positions, p.rope);
   __syncthreads();
   const bool in_rot = g < (p.rope.rot_dim >> 4);
-  float2 cs[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = in_rot ? turns[tk][8 * g + i] : make_float2(1.f, 0.f);
+  const RopeTurns cs = table.group(tk, in_rot ? g : 0);
   for (int h0 = hl; h0 < heads; h0 += 2 * HL) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -165,10 +158,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   constexpr int UT = W * 32;               // threads per unit
   constexpr int RL = UT / NG;              // rows side by side
   constexpr int CAP = RL * kRowsPerThread;  // rows held in registers
-  __shared__ float2 turns[kQTokens][D / 2];
+  __shared__ RopeTable<kQTokens, D / 2> table;
   __shared__ unsigned warp_max[kThreads / 32];
   if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {
-    turn_queries<D>(p, turns);
+    turn_queries<D>(p, table);
     return;
   }
   const int tid = threadIdx.x;
@@ -200,17 +193,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   const int64_t blk_end = (static_cast<int64_t>(blk) + 1) << p.bs_log2;
   const int hi = blk_end < ctx ? static_cast<int>(blk_end) : ctx;
   if (lo >= hi) return;
+  // the block's id and old scale are read while the rows' loads are on their way
   const int id = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks + blk);
-  if (id < 0 || id >= p.num_blocks) {
-    if (ut == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
-    return;
-  }
   const int rows = hi - lo;
   const int r0 = lo & (bs - 1);
   const int64_t tok0 = begin + (lo - pos0);
-  float* scale_at = (is_v ? p.v_scales : p.k_scales) + static_cast<int64_t>(id) * p.num_kv_heads + g;
-  const float old = r0 ? __ldcg(scale_at) : 0.f;
-
   const int grp = ut % NG, rl = ut / NG;
   const int2 at = rope_vectors(grp, p.rope);
   const bool turned = !is_v && grp < (p.rope.rot_dim >> 4);
@@ -218,8 +205,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v : p.k) + tok0 * stride + g * D);
   const int64_t vstride = stride / 8;
 
+  unsigned long long rate[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) rate[e] = turned ? rope_rate(__ldg(p.rope.inv_freq + 8 * grp + e)) : 0;
+
   uint4 a[kRowsPerThread], b[kRowsPerThread];
-  auto load = [&](int base) {
+  auto fetch = [&](int base) {
 #pragma unroll
     for (int i = 0; i < kRowsPerThread; ++i) {
       const int r = base + rl + i * RL;
@@ -229,18 +220,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         b[i] = __ldg(src + r * vstride + at.y);
       }
     }
+  };
+  auto turn = [&](int base) {
     if (turned) {
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __ldg(p.rope.inv_freq + 8 * grp + e);
 #pragma unroll
       for (int i = 0; i < kRowsPerThread; ++i) {
         const int r = base + rl + i * RL;
         if (r < rows) {
           const int pos = __ldg(p.positions + tok0 + r);
-          float2 cs[8];
+          RopeTurns cs;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) cs[e] = rope_turn(pos, f[e], p.rope.amplitude);
+          for (int e = 0; e < 8; ++e) set_turn(cs, e, rope_turn(pos, rate[e], p.rope.amplitude));
           rope_group(a[i], b[i], cs, p.rope.interleaved != 0);
         }
       }
@@ -250,8 +240,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   // ---- largest finite magnitude of the new rows, and the block's scale -------------------
   const int chunks = (rows + CAP - 1) / CAP;
   unsigned acc = 0;
+  float* scale_at = nullptr;
+  float old = 0.f;
   for (int c = 0; c < chunks; ++c) {
-    load(c * CAP);
+    fetch(c * CAP);
+    if (c == 0) {
+      if (id < 0 || id >= p.num_blocks) {  // the same for the whole unit
+        if (ut == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+        return;
+      }
+      scale_at = (is_v ? p.v_scales : p.k_scales) + static_cast<int64_t>(id) * p.num_kv_heads + g;
+      old = r0 ? __ldcg(scale_at) : 0.f;
+    }
+    turn(c * CAP);
 #pragma unroll
     for (int i = 0; i < kRowsPerThread; ++i) {
       acc = finite_max2(finite_max2(acc, a[i].x), a[i].y);
@@ -287,7 +288,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
       }
     }
     if (c == 0) break;
-    load((c - 1) * CAP);
+    fetch((c - 1) * CAP);
+    turn((c - 1) * CAP);
   }
 
   // ---- rows that were in the block before, when its scale grew ------------------------------
@@ -302,10 +304,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 }
 
 template <int D>
-cudaError_t launch_d(AppendParams p, cudaStream_t stream) {
+cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
   const int bs = 1 << p.bs_log2;
   const int rows = p.max_new < bs ? p.max_new : bs;  // most new rows of one unit
   const int64_t units = static_cast<int64_t>(p.num_seqs) * p.span * 2 * p.num_kv_heads;
+  if (!q_here) p.num_q_heads = 0;
   p.q_ctas = p.num_q_heads > 0 ? (p.num_tokens + kQTokens - 1) / kQTokens : 0;
   // a warp holds 32 rows of 128 dims in registers: units of up to 32 rows take one warp
   // (a decode step's single row, blocks of 16 and 32), larger ones eight
@@ -353,7 +356,25 @@ cudaError_t launch_append_blockscale(const AppendLaunch& a, cudaStream_t stream)
   p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = a.cache.num_kv_heads;
   p.err = device_error_word();
-  return a.cache.head_dim == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
+  // Few tokens: one launch, whose first CTAs turn the queries. Many: the queries' own kernel
+  // (64 registers against the units' 128, so twice the warps stream them).
+  const bool q_here = a.num_tokens <= 8 * sm_count();
+  if (!q_here && a.num_q_heads > 0) {
+    RopeStoreLaunch q{};
+    q.q_out = a.q_out;
+    q.q = a.q;
+    q.q_out_stride = a.q_out_stride;
+    q.q_stride = a.q_stride;
+    q.positions = a.positions;
+    q.rope = a.rope;
+    q.num_tokens = a.num_tokens;
+    q.num_q_heads = a.num_q_heads;
+    q.head_dim = a.cache.head_dim;
+    const cudaError_t e = launch_rope_store(q, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return a.cache.head_dim == 128 ? launch_d<128>(p, q_here, stream)
+                                 : launch_d<64>(p, q_here, stream);
 }
 
 }  // namespace pa
