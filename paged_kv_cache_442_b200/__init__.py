@@ -4,7 +4,8 @@ Argument marshalling only: every function here checks tensor dtypes/devices,
 turns torch tensors into device pointers and calls the C entry point of the same
 name (declared in include/pa.h). All arithmetic runs in the library's CUDA
 kernels; there is no CPU or PyTorch fallback. If libpa.so is missing or cannot be
-loaded, the first call raises.
+loaded, the first call raises. The rotary and block-scale entry points are marshalled by a
+compiled module (_pa_torch.so, csrc/torch/binding.cpp), the others through ctypes.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libpa.so")
+BINDING_PATH = os.path.join(PKG_DIR, "_pa_torch.so")
 
 PA_OK = 0
 STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_BAD_INDEX",
@@ -155,15 +157,32 @@ def load_library(path: str | None = None):
 
 
 # ----------------------------------------------------------------- marshalling
-_torch_module = None
-
-
 def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
+    import torch
+    return torch
+
+
+_native_module = None
+
+
+def _native():
+    """The compiled marshalling of the rotary and block-scale entry points (loaded once):
+    checks the tensors and calls libpa.so. Raises if it is missing: there is no fallback."""
+    global _native_module
+    if _native_module is None:
+        import importlib.machinery
+        import importlib.util
+        load_library()
+        _torch()   # its libraries first
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"{BINDING_PATH} not found: build it with "
+                              "`python -m paged_kv_cache_442_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_pa_torch", BINDING_PATH)
+        spec = importlib.util.spec_from_loader("_pa_torch", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _native_module = module
+    return _native_module
 
 
 def _check(t, name, dtype, ndim=None):
@@ -317,60 +336,6 @@ def pa_decode_fp8(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, co
     _raise("pa_decode_fp8", st)
 
 
-def _dense(dev, dtype, *named):
-    """Each (tensor, name, ndim) is a dense CUDA tensor of `dtype` on device `dev`: one pass of
-    cheap queries, since a decode step's launch takes less time than its checks could; _check
-    names what is wrong."""
-    torch = _torch()
-    for t, name, ndim in named:
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
-                and t.is_contiguous() and t.dim() == ndim):
-            _check(t, name, dtype, ndim)
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-
-
-def _rows(dev, t, name, num_tokens=None, shape=None):
-    """A bf16 tensor [tokens, heads, dim] on device `dev` whose tokens' rows are dense (the
-    tokens may be any multiple of 8 values apart: a slice of a fused projection). Returns its
-    shape and token stride."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    got = tuple(t.shape)
-    if len(got) != 3:
-        raise ValueError(f"{name} must have 3 dims, got {len(got)}")
-    if (num_tokens is not None and got[0] != num_tokens) or (shape is not None and got[1:] != shape):
-        raise ValueError(f"{name} has shape {got}, expected "
-                         f"[{num_tokens if num_tokens is not None else 'tokens'}, "
-                         f"{', '.join(map(str, shape)) if shape is not None else 'heads, dim'}]")
-    tokens, heads, dim = got
-    st, sh, sd = t.stride()
-    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim):
-        raise ValueError(f"{name}: each token's heads must be contiguous")
-    return got, st if tokens > 1 else -(-heads * dim // 8) * 8
-
-
-def _here(stream):
-    """The current device and the stream to launch on (an int for ctypes)."""
-    cuda = _torch()._C
-    dev = cuda._cuda_getDevice()
-    if stream is None:
-        return dev, cuda._cuda_getCurrentRawStream(dev)
-    return dev, stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _rope_desc(dev, inv_freq, interleaved, amplitude):
-    _dense(dev, _torch().float32, (inv_freq, "inv_freq", 1))
-    n = inv_freq.shape[0]
-    return pa_rope_desc(inv_freq.data_ptr() if n else None, 2 * n, 1 if interleaved else 0, amplitude)
-
-
 def pa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "none",
                      factor: float = 1.0, original_context: float = 0.0, beta_fast: float = 32.0,
                      beta_slow: float = 1.0):
@@ -392,95 +357,19 @@ def pa_rope(out, x, positions, inv_freq, interleaved: bool = False, amplitude: f
             stream=None) -> None:
     """out[t, h] = x[t, h] turned by positions[t] (out may be x): the first
     2 * len(inv_freq) dims of each head, the others copied. Tokens may be strided."""
-    lib = load_library()
-    _need_cuda(x, "x")
-    dev, raw = _here(stream)
-    (T, H, D), xs = _rows(dev, x, "x")
-    _, os_ = _rows(dev, out, "out", T, (H, D))
-    _dense(dev, _torch().int32, (positions, "positions", 1))
-    if positions.shape[0] != T:
-        raise ValueError("positions must be [num_tokens]")
-    st = lib.pa_rope(out.data_ptr(), os_, x.data_ptr(), xs, T, H, D, positions.data_ptr(),
-                     _rope_desc(dev, inv_freq, interleaved, amplitude), raw)
-    _raise("pa_rope", st)
-
-
-def _need_cuda(t, name):
-    """Refuse a CPU tensor before the current device is asked for (there may be none)."""
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-
-
-def _step_rows(dev, q_out, q, k, v, kv_shape):
-    """Of a step's q_out, q (may both be None), k and v: the tokens, the query heads, and the
-    pointers with their token strides in the C order."""
-    (T, _, _), ks = _rows(dev, k, "k", None, kv_shape)
-    _, vs = _rows(dev, v, "v", T, kv_shape)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
-    if q is None:
-        return T, 0, (None, 0, None, 0, k.data_ptr(), ks, v.data_ptr(), vs)
-    (_, hq, d), qs = _rows(dev, q, "q", T)
-    if d != kv_shape[1]:
-        raise ValueError("q and k must have the same head dim")
-    _, qos = _rows(dev, q_out, "q_out", T, (hq, d))
-    return T, hq, (q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs)
+    st = _native().rope(out, x, positions, inv_freq, interleaved, amplitude, stream)
+    if st:
+        _raise("pa_rope", st)
 
 
 def pa_rope_store_kvcache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq,
                           interleaved: bool = False, amplitude: float = 1.0, stream=None) -> None:
     """q_out = rotated q; rotated k and v stored at slot_mapping (-1 skips): one launch. q, k
     and v may be slices of one projection; q_out may be q; q and q_out may be None."""
-    torch = _torch()
-    lib = load_library()
-    _need_cuda(k, "k")
-    dev, raw = _here(stream)
-    _dense(dev, torch.bfloat16, (k_cache, "k_cache", 4), (v_cache, "v_cache", 4))
-    nb, bs, hkv, d = pool = tuple(k_cache.shape)
-    if tuple(v_cache.shape) != pool:
-        raise ValueError("k_cache/v_cache shapes must match")
-    T, hq, rows = _step_rows(dev, q_out, q, k, v, (hkv, d))
-    _dense(dev, torch.int32, (slot_mapping, "slot_mapping", 1), (positions, "positions", 1))
-    if slot_mapping.shape[0] != T or positions.shape[0] != T:
-        raise ValueError("slot_mapping and positions must be [num_tokens]")
-    st = lib.pa_rope_store_kvcache(*rows, k_cache.data_ptr(), v_cache.data_ptr(),
-                                   pa_cache_desc(nb, bs, hkv, d), slot_mapping.data_ptr(), T, hq,
-                                   positions.data_ptr(),
-                                   _rope_desc(dev, inv_freq, interleaved, amplitude), raw)
-    _raise("pa_rope_store_kvcache", st)
-
-
-def _blockscale_pools(dev, k_codes, v_codes, k_scales, v_scales):
-    """The pools' shape, after the checks every block-scale call makes of them."""
-    torch = _torch()
-    _dense(dev, torch.uint8, (k_codes, "k_codes", 4), (v_codes, "v_codes", 4))
-    _dense(dev, torch.float32, (k_scales, "k_scales", 2), (v_scales, "v_scales", 2))
-    pool = tuple(k_codes.shape)
-    if tuple(v_codes.shape) != pool:
-        raise ValueError("K and V pools must have the same shapes")
-    want = (pool[0], pool[2])
-    if tuple(k_scales.shape) != want or tuple(v_scales.shape) != want:
-        raise ValueError("scales must be [num_blocks, num_kv_heads] fp32")
-    return pool
-
-
-def _append(fn, name, dev, raw, q_out, q, k, v, k_codes, v_codes, k_scales, v_scales, block_tables,
-            cu_seqlens_q, context_lens, max_q_len, tail):
-    torch = _torch()
-    nb, bs, hkv, d = _blockscale_pools(dev, k_codes, v_codes, k_scales, v_scales)
-    T, hq, rows = _step_rows(dev, q_out, q, k, v, (hkv, d))
-    _dense(dev, torch.int32, (block_tables, "block_tables", 2), (cu_seqlens_q, "cu_seqlens_q", 1),
-           (context_lens, "context_lens", 1))
-    B, width = block_tables.shape
-    if cu_seqlens_q.shape[0] != B + 1 or context_lens.shape[0] != B:
-        raise ValueError("cu_seqlens_q/block_tables/context_lens disagree on num_seqs")
-    st = fn(*(rows if tail is not None else rows[4:]), k_codes.data_ptr(), v_codes.data_ptr(),
-            k_scales.data_ptr(), v_scales.data_ptr(), pa_cache_desc(nb, bs, hkv, d),
-            block_tables.data_ptr(), width, cu_seqlens_q.data_ptr(), context_lens.data_ptr(), B, T,
-            max_q_len, *((hq, *tail(T)) if tail is not None else ()), raw)
-    _raise(name, st)
+    st = _native().rope_store_kvcache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
+                                      inv_freq, interleaved, amplitude, stream)
+    if st:
+        _raise("pa_rope_store_kvcache", st)
 
 
 def pa_store_kvcache_fp8_blockscale(k, v, k_codes, v_codes, k_scales, v_scales, block_tables,
@@ -489,12 +378,10 @@ def pa_store_kvcache_fp8_blockscale(k, v, k_codes, v_codes, k_scales, v_scales, 
     """Append each sequence's new rows (the last ones of its context) to e4m3 pools with one
     fp32 scale per (block, kv head): codes uint8 [num_blocks, bs, Hkv, D], scales fp32
     [num_blocks, Hkv]. A block's scale grows with its rows (include/pa.h)."""
-    lib = load_library()
-    _need_cuda(k, "k")
-    dev, raw = _here(stream)
-    _append(lib.pa_store_kvcache_fp8_blockscale, "pa_store_kvcache_fp8_blockscale", dev, raw, None,
-            None, k, v, k_codes, v_codes, k_scales, v_scales, block_tables, cu_seqlens_q,
-            context_lens, max_q_len, None)
+    st = _native().store_blockscale(k, v, k_codes, v_codes, k_scales, v_scales, block_tables,
+                                    cu_seqlens_q, context_lens, max_q_len, stream)
+    if st:
+        _raise("pa_store_kvcache_fp8_blockscale", st)
 
 
 def pa_rope_store_kvcache_fp8_blockscale(q_out, q, k, v, k_codes, v_codes, k_scales, v_scales,
@@ -502,20 +389,12 @@ def pa_rope_store_kvcache_fp8_blockscale(q_out, q, k, v, k_codes, v_codes, k_sca
                                          positions, inv_freq, interleaved: bool = False,
                                          amplitude: float = 1.0, stream=None) -> None:
     """q_out = rotated q, then pa_store_kvcache_fp8_blockscale of the rotated k and of v, with
-    the same bits in one call."""
-    lib = load_library()
-    _need_cuda(k, "k")
-    dev, raw = _here(stream)
-
-    def tail(T):
-        _dense(dev, _torch().int32, (positions, "positions", 1))
-        if positions.shape[0] != T:
-            raise ValueError("positions must be [num_tokens]")
-        return positions.data_ptr(), _rope_desc(dev, inv_freq, interleaved, amplitude)
-
-    _append(lib.pa_rope_store_kvcache_fp8_blockscale, "pa_rope_store_kvcache_fp8_blockscale", dev,
-            raw, q_out, q, k, v, k_codes, v_codes, k_scales, v_scales, block_tables, cu_seqlens_q,
-            context_lens, max_q_len, tail)
+    the same bits in one call. q and q_out may be None."""
+    st = _native().rope_store_blockscale(q_out, q, k, v, k_codes, v_codes, k_scales, v_scales,
+                                         block_tables, cu_seqlens_q, context_lens, max_q_len,
+                                         positions, inv_freq, interleaved, amplitude, stream)
+    if st:
+        _raise("pa_rope_store_kvcache_fp8_blockscale", st)
 
 
 def pa_decode_fp8_blockscale_workspace_size(num_q_heads: int, num_kv_heads: int) -> int:
@@ -535,26 +414,10 @@ def pa_decode_fp8_blockscale(out, q, k_codes, v_codes, k_scales, v_scales, block
                              stream=None) -> None:
     """Paged decode attention over e4m3 pools with block scales into `out` [num_seqs, Hq, D]
     (bf16). workspace: decode_fp8_blockscale_workspace."""
-    torch = _torch()
-    lib = load_library()
-    _need_cuda(q, "q")
-    dev, raw = _here(stream)
-    _dense(dev, torch.bfloat16, (out, "out", 3), (q, "q", 3))
-    nb, bs, hkv, d = _blockscale_pools(dev, k_codes, v_codes, k_scales, v_scales)
-    _dense(dev, torch.int32, (block_tables, "block_tables", 2), (context_lens, "context_lens", 1))
-    B, Hq, D = shape = tuple(q.shape)
-    rows, width = block_tables.shape
-    if tuple(out.shape) != shape or rows != B or context_lens.shape[0] != B:
-        raise ValueError("out/q/block_tables/context_lens disagree on num_seqs")
-    if D != d:
-        raise ValueError("q and the pools must have the same head dim")
-    _dense(dev, workspace.dtype, (workspace, "workspace", workspace.dim()))
-    st = lib.pa_decode_fp8_blockscale(
-        out.data_ptr(), q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
-        v_scales.data_ptr(), pa_cache_desc(nb, bs, hkv, d), block_tables.data_ptr(), width,
-        context_lens.data_ptr(), B, Hq, scale, max_context_len, workspace.data_ptr(),
-        workspace.nbytes, raw)
-    _raise("pa_decode_fp8_blockscale", st)
+    st = _native().decode_blockscale(out, q, k_codes, v_codes, k_scales, v_scales, block_tables,
+                                     context_lens, scale, max_context_len, workspace, stream)
+    if st:
+        _raise("pa_decode_fp8_blockscale", st)
 
 
 class BlockManager:

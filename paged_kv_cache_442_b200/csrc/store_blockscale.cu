@@ -20,15 +20,21 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <cooperative_groups.h>
+
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 #include "rope.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerThread = 8;  // rows a thread keeps in registers (64 registers)
+constexpr int kFewRows = 32;    // new rows of a block that one warp takes
+constexpr int kRowHeads = 8;    // (row, head) pairs a thread keeps in registers (64 registers)
+constexpr int kMaxCluster = 8;  // portable cluster size
 constexpr int kQTokens = 2;        // tokens of a CTA that turns queries
 
 struct AppendParams {
@@ -56,6 +62,7 @@ struct AppendParams {
   int num_q_heads;
   int num_kv_heads;
   int q_ctas;
+  int cluster;  // CTAs per block (append_many_kernel)
   unsigned* err;
 };
 
@@ -70,11 +77,16 @@ __device__ __forceinline__ float exp2_int(int k) {  // 2^k, k in [-126, 127]
   return __uint_as_float(static_cast<unsigned>(k + 127) << 23);
 }
 
-// Largest finite magnitude of both halves, kept per half (as bits).
+// Larger magnitude of both halves, kept per half (as bits, which order as the values do).
+__device__ __forceinline__ unsigned abs_max2(unsigned acc, unsigned w) {
+  return __vmaxu2(acc, w & 0x7fff7fffu);
+}
+// The same with infinities and NaN counted as 0 (bits from 0x7f80 on).
 __device__ __forceinline__ unsigned finite_max2(unsigned acc, unsigned w) {
   const unsigned m = w & 0x7fff7fffu;
   return __vmaxu2(acc, m & __vcmpltu2(m, 0x7f807f80u));
 }
+constexpr unsigned kInfBits = 0x7f80u;
 
 // Eight bf16 values times inv -> eight codes.
 __device__ __forceinline__ uint2 quantise8(const uint4& w, float inv) {
@@ -82,10 +94,10 @@ __device__ __forceinline__ uint2 quantise8(const uint4& w, float inv) {
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    c[i] = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fmul_rn(bf16lo_to_f32(x[i]), inv), __fmul_rn(bf16hi_to_f32(x[i]), inv)),
-        __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    c[i] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(bf16lo_to_f32(x[i]), bf16hi_to_f32(x[i])),
+                                               make_float2(inv, inv)),
+                                    __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 // Sixteen codes to the codes of the same values over a scale that is 1 / factor as large.
@@ -107,6 +119,24 @@ __device__ __forceinline__ uint4 requantise16(uint4 w, float factor) {
     x[i] = r;
   }
   return w;
+}
+
+// The first `rows` rows of a block's head, to a scale 1 / factor as large.
+template <int D>
+__device__ __forceinline__ void requantise_rows(uint8_t* codes, int64_t row_bytes, int rows,
+                                                float factor, int first, int step) {
+  constexpr int VPR = D / 16;  // 16-byte vectors of codes per row
+  for (int i = first; i < rows * VPR; i += step) {
+    uint4* at = reinterpret_cast<uint4*>(codes + (i / VPR) * row_bytes) + i % VPR;
+    *at = requantise16(*at, factor);
+  }
+}
+
+// The table's memory as rates of the frequencies (D / 2 of them) in CTAs without queries.
+template <int D2>
+__device__ __forceinline__ unsigned long long* rates_of(RopeTable<kQTokens, D2>& table) {
+  static_assert(sizeof(table) >= D2 * sizeof(unsigned long long), "rates fit the table");
+  return reinterpret_cast<unsigned long long*>(&table);
 }
 
 // The queries of kQTokens tokens (as in rope.cu).
@@ -152,21 +182,79 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p,
   }
 }
 
-template <int D, int W>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
-  constexpr int NG = D / 16;               // threads per row
-  constexpr int UT = W * 32;               // threads per unit
-  constexpr int RL = UT / NG;              // rows side by side
-  constexpr int CAP = RL * kRowsPerThread;  // rows held in registers
+// The new rows of one (sequence, j-th block they reach): `rows` rows from offset r0 of the
+// block, tokens tok0 ... false: nothing to do (or bad lengths, which `report` records).
+struct Span {
+  int id;  // physical block, unchecked
+  int rows, r0;
+  int64_t tok0;
+};
+
+__device__ __forceinline__ bool find_span(const AppendParams& p, int s, int j, bool report,
+                                          Span& u) {
+  const int begin = __ldg(p.cu_seqlens + s), end = __ldg(p.cu_seqlens + s + 1);
+  const int ctx = __ldg(p.context_lens + s);
+  const int n = end - begin;
+  if (begin < 0 || n < 0 || end > p.num_tokens || n > p.max_new || ctx < n ||
+      static_cast<int64_t>(ctx) > (static_cast<int64_t>(p.max_blocks) << p.bs_log2)) {
+    if (report) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+    return false;
+  }
+  if (n == 0) return false;
+  const int pos0 = ctx - n;
+  const int blk = (pos0 >> p.bs_log2) + j;
+  const int64_t start = static_cast<int64_t>(blk) << p.bs_log2;
+  const int64_t stop = start + (1ll << p.bs_log2);
+  const int lo = start > pos0 ? static_cast<int>(min(start, static_cast<int64_t>(ctx))) : pos0;
+  const int hi = stop < ctx ? static_cast<int>(stop) : ctx;
+  if (lo >= hi) return false;
+  // read while the rows' loads are on their way; checked by the caller after issuing them
+  u.id = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks + blk);
+  u.rows = hi - lo;
+  u.r0 = lo & ((1 << p.bs_log2) - 1);
+  u.tok0 = begin + (lo - pos0);
+  return true;
+}
+
+// Largest finite magnitude (bits) of N vectors.
+template <int N>
+__device__ __forceinline__ unsigned top_of(const uint4 (&a)[N], const uint4 (&b)[N]) {
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    top = abs_max2(abs_max2(top, a[i].x), a[i].y);
+    top = abs_max2(abs_max2(top, a[i].z), a[i].w);
+    top = abs_max2(abs_max2(top, b[i].x), b[i].y);
+    top = abs_max2(abs_max2(top, b[i].z), b[i].w);
+  }
+  if (max(top & 0xffffu, top >> 16) >= kInfBits) {  // rare: only finite values set the scale
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      top = finite_max2(finite_max2(top, a[i].x), a[i].y);
+      top = finite_max2(finite_max2(top, a[i].z), a[i].w);
+      top = finite_max2(finite_max2(top, b[i].x), b[i].y);
+      top = finite_max2(finite_max2(top, b[i].z), b[i].w);
+    }
+  }
+  return max(top & 0xffffu, top >> 16);
+}
+
+// Few new rows per block (a decode step; blocks of 16 and 32): a warp per (sequence, block,
+// K or V, head), eight to a CTA.
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams p) {
+  constexpr int NG = D / 16;         // threads per row
+  constexpr int RL = 32 / NG;        // rows side by side
+  constexpr int RT = kFewRows / RL;  // rows a thread keeps in registers (8 at 128 dims)
   __shared__ RopeTable<kQTokens, D / 2> table;
-  __shared__ unsigned warp_max[kThreads / 32];
   if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {
     turn_queries<D>(p, table);
     return;
   }
-  const int tid = threadIdx.x;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x - p.q_ctas) * (kThreads / UT) + tid / UT;
-  const int ut = tid % UT;
+  const int lane = threadIdx.x & 31;
+  const int64_t unit =
+      static_cast<int64_t>(blockIdx.x - p.q_ctas) * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t per_seq = static_cast<int64_t>(p.span) * 2 * p.num_kv_heads;
   if (unit >= per_seq * p.num_seqs) return;
   const int s = static_cast<int>(unit / per_seq);
@@ -174,154 +262,271 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
   const int g = rest % p.num_kv_heads;
   rest /= p.num_kv_heads;
   const bool is_v = rest & 1;
-  const int j = rest >> 1;
+  Span u;
+  if (!find_span(p, s, rest >> 1, lane == 0, u)) return;
 
-  // ---- the unit's rows: [r0, r0 + rows) of the block, tokens tok0 .. --------------------
-  const int begin = __ldg(p.cu_seqlens + s), end = __ldg(p.cu_seqlens + s + 1);
-  const int ctx = __ldg(p.context_lens + s);
-  const int bs = 1 << p.bs_log2;
-  const int n = end - begin;
-  if (begin < 0 || n < 0 || end > p.num_tokens || n > p.max_new || ctx < n ||
-      static_cast<int64_t>(ctx) > (static_cast<int64_t>(p.max_blocks) << p.bs_log2)) {
-    if (ut == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
-    return;
-  }
-  if (n == 0) return;
-  const int pos0 = ctx - n;
-  const int blk = (pos0 >> p.bs_log2) + j;
-  const int lo = max(pos0, blk << p.bs_log2);
-  const int64_t blk_end = (static_cast<int64_t>(blk) + 1) << p.bs_log2;
-  const int hi = blk_end < ctx ? static_cast<int>(blk_end) : ctx;
-  if (lo >= hi) return;
-  // the block's id and old scale are read while the rows' loads are on their way
-  const int id = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks + blk);
-  const int rows = hi - lo;
-  const int r0 = lo & (bs - 1);
-  const int64_t tok0 = begin + (lo - pos0);
-  const int grp = ut % NG, rl = ut / NG;
+  const int grp = lane % NG, rl = lane / NG;
   const int2 at = rope_vectors(grp, p.rope);
   const bool turned = !is_v && grp < (p.rope.rot_dim >> 4);
-  const int64_t stride = is_v ? p.v_stride : p.k_stride;
-  const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v : p.k) + tok0 * stride + g * D);
-  const int64_t vstride = stride / 8;
-
-  unsigned long long rate[8];
+  const int64_t vstride = (is_v ? p.v_stride : p.k_stride) / 8;
+  const uint4* src = reinterpret_cast<const uint4*>(is_v ? p.v : p.k) + (u.tok0 + rl) * vstride +
+                     g * (D / 8);
+  uint4 a[RT], b[RT];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) rate[e] = turned ? rope_rate(__ldg(p.rope.inv_freq + 8 * grp + e)) : 0;
-
-  uint4 a[kRowsPerThread], b[kRowsPerThread];
-  auto fetch = [&](int base) {
+  for (int i = 0; i < RT; ++i) {
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (rl + i * RL < u.rows) {
+      a[i] = __ldg(src + i * (RL * vstride) + at.x);
+      b[i] = __ldg(src + i * (RL * vstride) + at.y);
+    }
+  }
+  if (u.id < 0 || u.id >= p.num_blocks) {
+    if (lane == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+    return;
+  }
+  float* scale_at = (is_v ? p.v_scales : p.k_scales) + static_cast<int64_t>(u.id) * p.num_kv_heads + g;
+  const float old = u.r0 ? __ldcg(scale_at) : 0.f;
+  if (turned) {
+    unsigned long long rate[8];
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-      const int r = base + rl + i * RL;
-      a[i] = b[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        a[i] = __ldg(src + r * vstride + at.x);
-        b[i] = __ldg(src + r * vstride + at.y);
+    for (int e = 0; e < 8; ++e) rate[e] = rope_rate(__ldg(p.rope.inv_freq + 8 * grp + e));
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if (rl + i * RL < u.rows) {
+        const int pos = __ldg(p.positions + u.tok0 + rl + i * RL);
+        RopeTurns cs;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) set_turn(cs, e, rope_turn(pos, rate[e], p.rope.amplitude));
+        rope_group(a[i], b[i], cs, p.rope.interleaved != 0);
       }
     }
-  };
-  auto turn = [&](int base) {
-    if (turned) {
+  }
+  const unsigned amax = __reduce_max_sync(0xffffffffu, top_of(a, b));
+  const float need = exp2_int(scale_exponent(amax));
+  const float scale = old >= need ? old : need;  // old is 0 for a block that starts here
+  const float inv = __frcp_rn(scale);
+  if (lane == 0 && scale != old) *scale_at = scale;
+  uint8_t* codes = (is_v ? p.v_codes : p.k_codes) +
+                   ((static_cast<int64_t>(u.id) << p.bs_log2) * p.num_kv_heads + g) * D;
+  const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D;
 #pragma unroll
-      for (int i = 0; i < kRowsPerThread; ++i) {
-        const int r = base + rl + i * RL;
-        if (r < rows) {
-          const int pos = __ldg(p.positions + tok0 + r);
-          RopeTurns cs;
+  for (int i = 0; i < RT; ++i) {
+    if (rl + i * RL < u.rows) {
+      uint8_t* dst = codes + (u.r0 + rl + i * RL) * row_bytes;
+      *reinterpret_cast<uint2*>(dst + at.x * 8) = quantise8(a[i], inv);
+      *reinterpret_cast<uint2*>(dst + at.y * 8) = quantise8(b[i], inv);
+    }
+  }
+  // rows that were in the block before, when its scale grew
+  if (u.r0 > 0 && scale != old)
+    requantise_rows<D>(codes, row_bytes, u.r0, __fdiv_rn(old, scale), lane, 32);
+}
+
+// Many new rows per block: a cluster of CTAs per (sequence, block, K or V, HT heads). A CTA
+// takes kRowHeads / HT rows per thread of the block, each in HT heads, so that the turns of a
+// (row, frequency) are computed once for HT heads, and a row's HT heads (256 bytes each) are
+// read together. The CTAs of a cluster hold one block between them and exchange their largest
+// magnitudes through distributed shared memory before they quantise.
+template <int D, int HT>
+__global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendParams p) {
+  constexpr int NG = D / 16;
+  constexpr int RL = kThreads / NG;      // rows side by side
+  constexpr int RT = kRowHeads / HT;     // rows per thread
+  constexpr int CAP = RL * RT;           // rows of a CTA
+  __shared__ RopeTable<kQTokens, D / 2> table;
+  __shared__ unsigned warp_top[kThreads / 32][HT];
+  __shared__ unsigned cta_top[kMaxCluster][HT];
+  if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {  // whole clusters
+    turn_queries<D>(p, table);
+    return;
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = p.cluster, rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x;
+  const int64_t unit = (blockIdx.x - p.q_ctas) / ranks;
+  const int hgroups = p.num_kv_heads / HT;
+  const int64_t per_seq = static_cast<int64_t>(p.span) * 2 * hgroups;
+  const int s = static_cast<int>(unit / per_seq);
+  int rest = static_cast<int>(unit - s * per_seq);
+  const int g = rest % hgroups * HT;
+  rest /= hgroups;
+  const bool is_v = rest & 1;
+  Span u;
+  // (every return up to the exchange is taken by the whole cluster)
+  if (!find_span(p, s, rest >> 1, tid == 0 && rank == 0, u)) return;
+
+  const int grp = tid % NG, rl = tid / NG;
+  const int2 at = rope_vectors(grp, p.rope);
+  const bool turned = !is_v && grp < (p.rope.rot_dim >> 4);
+  const int64_t vstride = (is_v ? p.v_stride : p.k_stride) / 8;
+  const int mine = rank * CAP + rl;  // first row of this thread
+  const int step = ranks * CAP;      // rows of one pass of the cluster
+  const uint4* src = reinterpret_cast<const uint4*>(is_v ? p.v : p.k) + (u.tok0 + mine) * vstride +
+                     g * (D / 8);
+  uint4 a[kRowHeads], b[kRowHeads];
+  auto fetch = [&](int base) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) set_turn(cs, e, rope_turn(pos, rate[e], p.rope.amplitude));
-          rope_group(a[i], b[i], cs, p.rope.interleaved != 0);
+    for (int i = 0; i < RT; ++i) {
+      const uint4* row = src + base * vstride + i * (RL * vstride);
+      const bool in = base + mine + i * RL < u.rows;
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+        a[i * HT + h] = b[i * HT + h] = make_uint4(0, 0, 0, 0);
+        if (in) {
+          a[i * HT + h] = __ldg(row + h * (D / 8) + at.x);
+          b[i * HT + h] = __ldg(row + h * (D / 8) + at.y);
         }
       }
     }
   };
+  auto turn = [&](int base) {
+    if (!turned) return;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if (base + mine + i * RL >= u.rows) continue;
+      const int pos = __ldg(p.positions + u.tok0 + base + mine + i * RL);
+      RopeTurns cs;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        set_turn(cs, e, rope_turn(pos, rates_of(table)[8 * grp + e], p.rope.amplitude));
+#pragma unroll
+      for (int h = 0; h < HT; ++h) rope_group(a[i * HT + h], b[i * HT + h], cs, p.rope.interleaved != 0);
+    }
+  };
 
-  // ---- largest finite magnitude of the new rows, and the block's scale -------------------
-  const int chunks = (rows + CAP - 1) / CAP;
-  unsigned acc = 0;
-  float* scale_at = nullptr;
-  float old = 0.f;
-  for (int c = 0; c < chunks; ++c) {
-    fetch(c * CAP);
+  unsigned top[HT];
+#pragma unroll
+  for (int h = 0; h < HT; ++h) top[h] = 0;
+  float old[HT];
+  const int passes = (u.rows + step - 1) / step;  // 1 up to 8 CTAs' rows; more: read twice
+  const int64_t scale_row = static_cast<int64_t>(u.id) * p.num_kv_heads + g;
+  float* scales = is_v ? p.v_scales : p.k_scales;
+  for (int c = 0; c < passes; ++c) {
+    fetch(c * step);
     if (c == 0) {
-      if (id < 0 || id >= p.num_blocks) {  // the same for the whole unit
-        if (ut == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+      if (u.id < 0 || u.id >= p.num_blocks) {
+        if (tid == 0 && rank == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
         return;
       }
-      scale_at = (is_v ? p.v_scales : p.k_scales) + static_cast<int64_t>(id) * p.num_kv_heads + g;
-      old = r0 ? __ldcg(scale_at) : 0.f;
-    }
-    turn(c * CAP);
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-      acc = finite_max2(finite_max2(acc, a[i].x), a[i].y);
-      acc = finite_max2(finite_max2(acc, a[i].z), a[i].w);
-      acc = finite_max2(finite_max2(acc, b[i].x), b[i].y);
-      acc = finite_max2(finite_max2(acc, b[i].z), b[i].w);
+      for (int h = 0; h < HT; ++h) old[h] = u.r0 ? __ldcg(scales + scale_row + h) : 0.f;
+      // the rates of the frequencies, once per CTA (in the queries' table, unused here)
+      if (!is_v && tid < (p.rope.rot_dim >> 1))
+        rates_of(table)[tid] = rope_rate(__ldg(p.rope.inv_freq + tid));
+      __syncthreads();
+    }
+    turn(c * step);
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+      uint4 ah[RT], bh[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        ah[i] = a[i * HT + h];
+        bh[i] = b[i * HT + h];
+      }
+      top[h] = max(top[h], top_of(ah, bh));
     }
   }
-  unsigned amax = __reduce_max_sync(0xffffffffu, max(acc & 0xffffu, acc >> 16));
-  if constexpr (W > 1) {
-    if ((tid & 31) == 0) warp_max[tid >> 5] = amax;
-    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < W; ++w) amax = max(amax, warp_max[w]);
+  for (int h = 0; h < HT; ++h) {
+    const unsigned t = __reduce_max_sync(0xffffffffu, top[h]);
+    if ((tid & 31) == 0) warp_top[tid >> 5][h] = t;
   }
-  const float need = exp2_int(scale_exponent(amax));
-  const float scale = old >= need ? old : need;  // old is 0 for a block that starts here
-  const float inv = __frcp_rn(scale);
-  if (ut == 0 && scale != old) *scale_at = scale;
-
-  // ---- codes of the new rows -------------------------------------------------------------
+  __syncthreads();
+  if (ranks > 1) {
+    if (tid < ranks * HT) {  // this CTA's maximum of head h to rank r
+      const int r = tid / HT, h = tid % HT;
+      unsigned t = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) t = max(t, warp_top[w][h]);
+      *cluster.map_shared_rank(&cta_top[rank][h], r) = t;
+    }
+    cluster.sync();
+  }
+  float scale[HT];
+#pragma unroll
+  for (int h = 0; h < HT; ++h) {
+    unsigned t = 0;
+    if (ranks > 1) {
+      for (int r = 0; r < ranks; ++r) t = max(t, cta_top[r][h]);
+    } else {
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) t = max(t, warp_top[w][h]);
+    }
+    const float need = exp2_int(scale_exponent(t));
+    scale[h] = old[h] >= need ? old[h] : need;  // old is 0 for a block that starts here
+    if (tid == 0 && rank == 0 && scale[h] != old[h]) scales[scale_row + h] = scale[h];
+  }
   uint8_t* codes = (is_v ? p.v_codes : p.k_codes) +
-                   ((static_cast<int64_t>(id) << p.bs_log2) * p.num_kv_heads + g) * D;
+                   ((static_cast<int64_t>(u.id) << p.bs_log2) * p.num_kv_heads + g) * D;
   const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D;
-  for (int c = chunks - 1;; --c) {
+  for (int c = passes - 1;; --c) {
+    uint8_t* first = codes + (u.r0 + c * step + mine) * row_bytes;
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-      const int r = c * CAP + rl + i * RL;
-      if (r < rows) {
-        uint8_t* dst = codes + (r0 + r) * row_bytes;
-        *reinterpret_cast<uint2*>(dst + at.x * 8) = quantise8(a[i], inv);
-        *reinterpret_cast<uint2*>(dst + at.y * 8) = quantise8(b[i], inv);
+    for (int h = 0; h < HT; ++h) {
+      const float inv = __frcp_rn(scale[h]);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        if (c * step + mine + i * RL < u.rows) {
+          uint8_t* dst = first + i * (RL * row_bytes) + h * D;
+          *reinterpret_cast<uint2*>(dst + at.x * 8) = quantise8(a[i * HT + h], inv);
+          *reinterpret_cast<uint2*>(dst + at.y * 8) = quantise8(b[i * HT + h], inv);
+        }
       }
     }
     if (c == 0) break;
-    fetch((c - 1) * CAP);
-    turn((c - 1) * CAP);
+    fetch((c - 1) * step);
+    turn((c - 1) * step);
   }
+  if (u.r0 > 0) {
+#pragma unroll
+    for (int h = 0; h < HT; ++h)
+      if (scale[h] != old[h])
+        requantise_rows<D>(codes + h * D, row_bytes, u.r0, __fdiv_rn(old[h], scale[h]),
+                           rank * kThreads + tid, ranks * kThreads);
+  }
+}
 
-  // ---- rows that were in the block before, when its scale grew ------------------------------
-  if (r0 > 0 && scale != old) {
-    const float factor = __fdiv_rn(old, scale);
-    constexpr int VPR = D / 16;  // 16-byte vectors of codes per row
-    for (int i = ut; i < r0 * VPR; i += UT) {
-      uint4* at_row = reinterpret_cast<uint4*>(codes + (i / VPR) * row_bytes) + i % VPR;
-      *at_row = requantise16(*at_row, factor);
-    }
-  }
+template <int D, int HT>
+cudaError_t launch_many(AppendParams p, int rows, cudaStream_t stream) {
+  constexpr int CAP = kThreads / (D / 16) * (kRowHeads / HT);
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && p.cluster * CAP < rows) p.cluster *= 2;
+  p.q_ctas = (p.q_ctas + p.cluster - 1) / p.cluster * p.cluster;
+  const int64_t grid = p.q_ctas + static_cast<int64_t>(p.num_seqs) * p.span * 2 *
+                                      (p.num_kv_heads / HT) * p.cluster;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, append_many_kernel<D, HT>, p);
 }
 
 template <int D>
 cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
   const int bs = 1 << p.bs_log2;
-  const int rows = p.max_new < bs ? p.max_new : bs;  // most new rows of one unit
-  const int64_t units = static_cast<int64_t>(p.num_seqs) * p.span * 2 * p.num_kv_heads;
+  const int rows = p.max_new < bs ? p.max_new : bs;  // most new rows of one block
   if (!q_here) p.num_q_heads = 0;
   p.q_ctas = p.num_q_heads > 0 ? (p.num_tokens + kQTokens - 1) / kQTokens : 0;
-  // a warp holds 32 rows of 128 dims in registers: units of up to 32 rows take one warp
-  // (a decode step's single row, blocks of 16 and 32), larger ones eight
-  if (rows <= 32) {
+  p.cluster = 1;
+  if (rows <= kFewRows) {
+    const int64_t units = static_cast<int64_t>(p.num_seqs) * p.span * 2 * p.num_kv_heads;
     const int64_t grid = p.q_ctas + (units + kThreads / 32 - 1) / (kThreads / 32);
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    append_kernel<D, 1><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
-  } else {
-    const int64_t grid = p.q_ctas + units;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    append_kernel<D, 8><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
+    append_few_kernel<D><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
   }
-  return cudaGetLastError();
+  if (p.num_kv_heads % 4 == 0) return launch_many<D, 4>(p, rows, stream);
+  if (p.num_kv_heads % 2 == 0) return launch_many<D, 2>(p, rows, stream);
+  return launch_many<D, 1>(p, rows, stream);
 }
 
 }  // namespace
