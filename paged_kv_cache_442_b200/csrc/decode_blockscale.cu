@@ -18,18 +18,22 @@
 //     (about 2^-8 relative, with an absolute floor of 2^-18 against a largest P' of 2^3 to
 //     2^6); O = (O_hi + O_lo / 128) R / l.
 //
-// Work. Unit = a tile of 256 positions of one (sequence, kv head). CTAs work in groups of
-// 4, 2 or 1 (the largest that divides the kv heads): the members of a group walk the same
-// tiles for neighbouring kv heads, so rows of several heads (128 bytes each) are fetched
-// together. All (sequence, head group, tile) units in order are cut into equal runs, one per
-// group: every CTA ends at the same time, and a CTA takes at most two partial (sequence,
-// kv head) items (its first and its last). The CTA that completes the last part of an item
-// merges them, sixteen parts at a time.
+// Work. CTAs work in groups of 4, 2 or 1 (the largest that divides the kv heads): the members
+// of a group walk the same tiles of 256 positions for neighbouring kv heads, so rows of
+// several heads (128 bytes each) are fetched together (one head per group: 82 us against
+// 59.5 on batch 64). All tiles, ordered by (sequence, head group, position), are cut into
+// runs of equal cost, one per group: a tile costs 8, a context's last tile as many eighths as
+// it has positions (4 at least). So a CTA takes at most two partial (sequence, kv head) items,
+// its first and its last, and every CTA knows how many parts an item is in; the CTA that
+// completes the last part merges them, sixteen parts at a time. (A share of the tiles left in
+// short chunks for the CTAs that are done first gained nothing: batch 64 59.6 - 61.5 us with
+// an eighth to a quarter of them in chunks of 2 to 5, 70 us in chunks of one; an item's
+// epilogue takes longer than a tile.)
 //
 // Bound: HBM (every K/V code is read once). Roles, as in the bf16 decode but streaming whole
 // runs: warps 0-7 softmax (two groups, one position of a 256-position tile per thread),
-// 8-11 epilogue, 12 TMA producer, 13 tensor-core issuer, 14 scheduler. The scheduler
-// publishes each tile's block ids and scales through a ring of tile records.
+// 8-11 epilogue, 12 and 15 TMA producers of K and of V, 13 tensor-core issuer, 14 scheduler.
+// The scheduler publishes each tile's block ids and scales through a ring of tile records.
 //
 // Waits name an mbarrier phase by its parity, so a wait for phase n must know that phase
 // n - 1 is complete. Every ring here is waited on phase after phase by the same role; the
@@ -59,9 +63,10 @@ constexpr int NO = 2;          // O^T accumulators
 constexpr int kMaxBlk = 16;    // blocks of one tile (block size 16)
 constexpr int kTileBytes = TT * HD;
 constexpr int kHalf = TM * HD;
-constexpr int kThreads = 480;
+constexpr int kThreads = 512;
 constexpr int kSoftThreads = 256;
 constexpr int kFan = 16;       // parts merged at a time
+constexpr int kTileCost = 8;   // of a full tile, in units of 32 positions
 constexpr float kTarget = 3.f;  // a new reference puts the largest P' at 2^kTarget ...
 constexpr float kBound = 6.f;   // ... and it moves when one would pass 2^kBound (128 (P' - hi)
                                 // is then at most 256, inside e4m3's 448)
@@ -84,15 +89,13 @@ struct TileRec {
   int item_s, item_g;  // item: sequence, kv head
   int part, nparts;    // this item's part of the (sequence, kv head)
   int group0;          // group holding part 0
-  int slot0;           // partial slot (0 or 1) of part 0 in its CTA
-  int which;           // this part's slot
-  int pad[2];
+  int pad[4];
 };
 static_assert(sizeof(TileRec) == 256, "tile record");
 
 // what the epilogue needs of an item
 struct ItemRec {
-  int s, g, part, nparts, group0, slot0, which, stop;
+  int s, g, part, nparts, group0, stop, pad[2];
 };
 static_assert(sizeof(ItemRec) == 32, "item record");
 
@@ -115,7 +118,9 @@ struct Cfg {
   static constexpr int kOffQs = round_up(kOffRed + 3 * 8 * G * 4, 16);
   static constexpr int kEpiBytes = 32 + 36 * 4;  // item record, m and l per head, R
   static constexpr int kOffEpi = round_up(kOffQs + QN * G * 4, 16);
-  static constexpr int kOffBar = round_up(kOffEpi + NO * kEpiBytes, 16);
+  // heads shared by several epilogue warps meet here when parts are merged
+  static constexpr int kOffMerge = round_up(kOffEpi + NO * kEpiBytes, 16);
+  static constexpr int kOffBar = kOffMerge + (G < 4 ? 4 * (HD + 4) * 4 : 0);
   static constexpr int kNumBars = 3 * ND + 2 * NK + 2 * NV + 2 * NS + 2 * NP + 2 * QN + 4 * NO + 1;
   static constexpr int kOffMisc = round_up(kOffBar + 8 * kNumBars, 16);
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
@@ -127,7 +132,8 @@ struct Cfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kQBytes % 1024 == 0 && kPChunk % 1024 == 0,
                 "swizzled operands");
-  static_assert(kOffRec % 16 == 0 && kOffBar % 8 == 0 && kOffEpi % 16 == 0, "alignment");
+  static_assert(kOffRec % 16 == 0 && kOffBar % 8 == 0 && kOffEpi % 16 == 0 && kOffMerge % 16 == 0,
+                "alignment");
   static_assert(NP <= NV, "the softmax's wait for a V tile relies on it (see the top)");
 };
 
@@ -138,9 +144,9 @@ struct BsParams {
   const float* v_scales;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  unsigned long long* counters;  // [2 * grid] first merge level, [2 * grid] second
-  float* ws_o;                   // [4 * grid][G][128]: partials, then the first level's results
-  float* ws_ml;                  // [4 * grid][G][2]
+  unsigned long long* counters;  // [2 * slots] arrivals
+  float* ws_o;                   // [slots][G][128] partials, slots = 2 * grid
+  float* ws_ml;                  // [slots][G][2]
   unsigned* err;
   unsigned long long tag;
   unsigned long long wait_ns;
@@ -154,6 +160,12 @@ struct BsParams {
   int max_context_len;
   float scale_log2;
 };
+
+__device__ __forceinline__ unsigned long long load_acquire(const unsigned long long* at) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ float warp_max(float v) {
   float r;
@@ -188,54 +200,74 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float (&v)[N]) {
   else tmem_st32(taddr, v);
 }
 
-// One merge step over `cnt` parts: part i's record is at slot_of(i). Thread dl owns output
-// dim dl; l and the unnormalised sums are combined under the largest maximum. Reads bypass
-// L1 (the parts were written by other SMs).
+// One merge step over cnt <= kFan parts, part i at slot_of(i), by the four epilogue warps: a
+// warp takes whole heads (G >= 4) or a head's parts in turn with 4 / G - 1 other warps. Lane i
+// reads part i's maximum and sum; the lanes hold 4 output dims each, so a part's row is one
+// 16-byte load per lane, and all of a head's loads are in flight together. Reads bypass L1
+// (the parts were written by other SMs). put(h, dim, M, L, A): head h, dims dim .. dim + 3.
 template <int G, class SlotOf, class Put>
-__device__ __forceinline__ void merge_parts(const BsParams& p, int cnt, int dl, SlotOf slot_of,
-                                            Put put) {
-  constexpr int CH = G <= 2 ? 8 : G <= 4 ? 4 : 2;  // parts in flight per head
-  float M[G], L[G], A[G];
-#pragma unroll
-  for (int h = 0; h < G; ++h) {
-    M[h] = -INFINITY;
-    L[h] = 0.f;
-    A[h] = 0.f;
-  }
+__device__ __forceinline__ void merge_parts(const BsParams& p, int cnt, int warp4, int lane,
+                                            float* buf, SlotOf slot_of, Put put) {
+  constexpr int S = G >= 4 ? 1 : 4 / G;  // warps that share a head
+  constexpr int N = kFan / S;            // parts of one warp
+  const int sub = G >= 4 ? 0 : warp4 / G;
 #pragma unroll 1
-  for (int c0 = 0; c0 < cnt; c0 += CH) {
-    float2 ml[CH][G];
-    float o[CH][G];
+  for (int h = G >= 4 ? warp4 : warp4 % G; h < G; h += 4) {
+    const int part = lane * S + sub;  // lane i holds the warp's i-th part
+    const bool in = lane < N && part < cnt;
+    const float2 ml = in ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(part) * G + h)
+                         : make_float2(-INFINITY, 0.f);
+    float4 o[N];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const bool in = c0 + i < cnt;
-      const int64_t slot = slot_of(in ? c0 + i : 0);
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        ml[i][h] = in ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot * G + h)
-                      : make_float2(-INFINITY, 0.f);
-        o[i][h] = in ? __ldcg(p.ws_o + (slot * G + h) * HD + dl) : 0.f;
-      }
+    for (int i = 0; i < N; ++i) {
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i * S + sub < cnt)
+        o[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (slot_of(i * S + sub) * G + h) * HD) + lane);
     }
+    float M = warp_max(ml.x);
+    float f = M > -INFINITY ? ex2_approx(ml.x - M) : 0.f;
+    float L = ml.y * f;
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      float mc = M[h];
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < CH; ++i) mc = fmaxf(mc, ml[i][h].x);
-      const float r = ex2_approx(M[h] - mc);  // 0 for the first chunk; every part has a finite max
-      L[h] *= r;
-      A[h] *= r;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const float f = ex2_approx(ml[i][h].x - mc);
-        L[h] += ml[i][h].y * f;
-        A[h] += o[i][h] * f;
-      }
-      M[h] = mc;
+    for (int i = 0; i < N; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      A.x = fmaf(fi, o[i].x, A.x);
+      A.y = fmaf(fi, o[i].y, A.y);
+      A.z = fmaf(fi, o[i].z, A.z);
+      A.w = fmaf(fi, o[i].w, A.w);
     }
+    if constexpr (S > 1) {
+      // the warps of a head meet in shared memory; the first one finishes
+      float* mine = buf + warp4 * (HD + 4);
+      reinterpret_cast<float4*>(mine)[lane] = A;
+      if (lane == 0) {
+        mine[HD] = M;
+        mine[HD + 1] = L;
+      }
+      named_bar_sync(2, 128);
+      if (sub == 0) {
+        float mx = M;
+#pragma unroll
+        for (int w = 1; w < S; ++w) mx = fmaxf(mx, buf[(warp4 + w * G) * (HD + 4) + HD]);
+        const float r = ex2_approx(M - mx);  // the first warp has part 0: M is finite
+        L *= r;
+        A = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
+#pragma unroll
+        for (int w = 1; w < S; ++w) {
+          const float* other = buf + (warp4 + w * G) * (HD + 4);
+          const float4 B = reinterpret_cast<const float4*>(other)[lane];
+          const float q = ex2_approx(other[HD] - mx);  // 0 for a warp without parts
+          L = fmaf(q, other[HD + 1], L);
+          A = make_float4(fmaf(q, B.x, A.x), fmaf(q, B.y, A.y), fmaf(q, B.z, A.z), fmaf(q, B.w, A.w));
+        }
+        M = mx;
+      }
+      named_bar_sync(2, 128);  // before the buffer's next use
+    }
+    if (sub == 0) put(h, 4 * lane, M, L, A);
   }
-#pragma unroll
-  for (int h = 0; h < G; ++h) put(h, M[h], L[h], A[h]);
 }
 
 template <int G>
@@ -257,9 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned long long wl = p.wait_ns;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* rec_full = bars;            // [ND] block ids of a tile -> producer, issuer, softmax
+  uint64_t* rec_full = bars;            // [ND] block ids of a tile -> producers, issuer, softmax
   uint64_t* scl_full = rec_full + ND;   // [ND] its scales -> softmax
-  uint64_t* rec_empty = scl_full + ND;  // [ND] producer, issuer and softmax are done with it
+  uint64_t* rec_empty = scl_full + ND;  // [ND] producers, issuer and softmax are done with it
   uint64_t* k_full = rec_empty + ND;    // [NK] TMA -> issuer
   uint64_t* k_empty = k_full + NK;      // [NK] score product done -> producer
   uint64_t* v_full = k_empty + NK;      // [NV] TMA -> issuer (+ softmax on a last tile)
@@ -286,27 +318,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int group = blockIdx.x / p.members;
   const int hgroups = p.num_kv_heads / p.members;
 
-  // The scheduler warp counts the tiles and finds its run before the set-up barrier, so
-  // that the context lengths' latency overlaps the set-up.
-  unsigned long long units = 0, u0 = 0, u1 = 0;
-  int groups = 1;
-  auto tiles_of = [&](int s) -> int {
+  // Scheduler warp state. The costs of 32 sequences at a time (one head group's) sit in the
+  // lanes (sequence seq0 + lane) with their running sums; runs only move forward, so the
+  // window does too.
+  int seq0 = 0, wctx = 0;
+  unsigned wcost = 0, winc = 0, wtotal = 0, wbase = 0;  // wbase: cost before the window
+  auto context = [&](int s) -> int {
     if (s >= p.num_seqs) return 0;
-    int ctx = __ldg(p.context_lens + s);
-    ctx = ctx > p.max_context_len ? p.max_context_len : ctx;
-    return ctx > 0 ? (ctx + TT - 1) / TT : 0;
+    const int ctx = __ldg(p.context_lens + s);
+    if (ctx > p.max_context_len) {
+      flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+      return p.max_context_len;
+    }
+    return ctx > 0 ? ctx : 0;
   };
-  if (warp == 14) {
-    unsigned long long sum = 0;
-#pragma unroll 4
-    for (int s = lane; s < p.num_seqs; s += 32) sum += tiles_of(s);
+  auto cost_of = [&](int ctx) -> unsigned {
+    if (ctx == 0) return 0;
+    const int tiles = (ctx + TT - 1) / TT;
+    const int tail = (ctx - (tiles - 1) * TT + 31) / 32;
+    return static_cast<unsigned>((tiles - 1) * kTileCost + (tail > kTileCost / 2 ? tail : kTileCost / 2));
+  };
+  auto window = [&]() {
+    wctx = context(seq0 + lane);
+    wcost = winc = cost_of(wctx);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    units = sum * hgroups;
-    groups = units < static_cast<unsigned long long>(p.groups) ? static_cast<int>(units) : p.groups;
-    if (group < groups) {
-      u0 = units * group / groups;
-      u1 = units * (group + 1) / groups;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned up = __shfl_up_sync(0xffffffffu, winc, o);
+      if (lane >= o) winc += up;
+    }
+    wtotal = __shfl_sync(0xffffffffu, winc, 31) * hgroups;
+  };
+  // the current item: sequence, head group, context, its cost and the cost before it
+  int it_s = 0, it_hg = 0, it_ctx = 0;
+  unsigned it_cost = 0, it_cum = 0;
+  auto pick = [&](unsigned c) {  // the item that holds cost c
+    while (wbase + wtotal <= c) {
+      wbase += wtotal;
+      seq0 += 32;
+      window();
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, wbase + winc * hgroups > c)) - 1;
+    it_cost = __shfl_sync(0xffffffffu, wcost, at);
+    it_ctx = __shfl_sync(0xffffffffu, wctx, at);
+    const unsigned before = wbase + (__shfl_sync(0xffffffffu, winc, at) - it_cost) * hgroups;
+    it_s = seq0 + at;
+    it_hg = static_cast<int>((c - before) / it_cost);
+    it_cum = before + it_hg * it_cost;
+  };
+  // group i takes the tiles that start in [run_start(i), run_start(i + 1))
+  unsigned cost = 0, run_q = 0, run_r = 0;
+  auto run_start = [&](unsigned i) { return i * run_q + (i < run_r ? i : run_r); };
+  auto group_of = [&](unsigned c) -> int {
+    const unsigned wide = run_r * (run_q + 1);
+    return c < wide ? c / (run_q + 1) : run_r + (c - wide) / run_q;
+  };
+  // block ids of 32 blocks from bb on
+  int bb = 0, bid = 0;
+  auto load_ids = [&](int b0) {
+    bb = b0;
+    const int b = b0 + lane;
+    bid = -1;
+    if ((b << p.bs_log2) < it_ctx && b < p.max_blocks)
+      bid = __ldg(p.block_tables + static_cast<int64_t>(it_s) * p.max_blocks + b);
+  };
+  // The scheduler counts the costs and reads its first block ids before the set-up barrier,
+  // so that these dependent reads overlap the set-up.
+  unsigned run_end = 0;
+  int first_tile = 0;
+  if (warp == 14) {
+    window();
+    cost = wtotal;
+    if (p.num_seqs > 32) {
+      unsigned sum = 0;
+#pragma unroll 2
+      for (int s = 32 + lane; s < p.num_seqs; s += 32) sum += cost_of(context(s));
+      cost += __reduce_add_sync(0xffffffffu, sum) * hgroups;
+    }
+    // runs at least a tile long: no run is skipped between two tiles of an item
+    const unsigned most = cost / kTileCost;
+    const unsigned groups = most < static_cast<unsigned>(p.groups) ? (most ? most : 1) : p.groups;
+    if (cost > 0 && static_cast<unsigned>(group) < groups) {
+      run_q = cost / groups;
+      run_r = cost - run_q * groups;
+      const unsigned start = run_start(group);
+      run_end = run_start(group + 1);
+      pick(start);
+      first_tile = static_cast<int>((start - it_cum + kTileCost - 1) / kTileCost);
+      if (first_tile * TT >= it_ctx) {  // the run starts inside the item's last tile
+        first_tile = 0;
+        if (it_cum + it_cost < run_end) pick(it_cum + it_cost);
+        else run_end = 0;
+      }
+      if (run_end) load_ids((first_tile * TT) >> p.bs_log2);
     }
   }
 
@@ -314,40 +417,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = tid; i < (QN * C::kQBytes + NP * C::kPBytes) / 16; i += kThreads)
     reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  if (tid == 0) {
-    for (int i = 0; i < ND; ++i) {
-      mbar_init(&rec_full[i], 1);
-      mbar_init(&scl_full[i], 1);
-      mbar_init(&rec_empty[i], 2 + kSoftThreads / 32);
-    }
-    for (int i = 0; i < NK; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < NV; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], kSoftThreads / 32);
-    }
-    for (int i = 0; i < NP; ++i) {
-      mbar_init(&p_full[i], kSoftThreads / 32);
-      mbar_init(&pv_done[i], 1);
-    }
-    for (int i = 0; i < QN; ++i) {
-      mbar_init(&q_ready[i], 1);
-      mbar_init(&q_empty[i], 2);
-    }
-    for (int i = 0; i < NO; ++i) {
-      mbar_init(&o_full[i], 1);
-      mbar_init(&o_free[i], 4);
-      mbar_init(&epi_full[i], 1);
-      mbar_init(&epi_empty[i], 1);
-    }
-    mbar_init(mma_drain, 1);
-    *abort_flag = 0;
+  if (tid < C::kNumBars) {
+    uint64_t* bar = bars + tid;
+    auto in = [&](uint64_t* first, int n) { return bar >= first && bar < first + n; };
+    const unsigned count = in(rec_empty, ND)                      ? 3 + kSoftThreads / 32
+                           : in(s_free, NS) || in(p_full, NP)     ? kSoftThreads / 32
+                           : in(q_empty, QN)                      ? 2
+                           : in(o_free, NO)                       ? 4
+                                                                  : 1;
+    mbar_init(bar, count);
+    if (tid == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 13) {
@@ -359,104 +438,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 12) {
-    // ======================================================== TMA producer
-    if (lane == 0) {
-      prefetch_tensormap(&tmK);
-      prefetch_tensormap(&tmV);
-    }
+  if (warp == 12 || warp == 15) {
+    // ======================================================== TMA producers (K: 12, V: 15)
+    const bool is_v = warp == 15;
+    const CUtensorMap* map = is_v ? &tmV : &tmK;
+    const CUtensorMap* map_tail = is_v ? &tmVt : &tmKt;
+    uint8_t* ring = smem + (is_v ? C::kOffV : C::kOffK);
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
+    static_assert(NK == NV, "one ring depth");
+    if (lane == 0) prefetch_tensormap(map);
     __syncwarp();
     const int rows = bs < TT ? bs : TT;    // rows per box of a full tile
     const int trows = bs < 32 ? bs : 32;   // of a context's last tile (no rows past it)
-    unsigned jk = 0, jv = 0;  // K and V tiles whose loads were started
+    unsigned j = 0;  // tiles whose loads were started
     while (true) {
-      const int rs = jk % ND;
-      if (!warp_wait_or_abort(&rec_full[rs], (jk / ND) & 1, p.err, abort_flag, wl)) break;
+      const int rs = j % ND, slot = j % NK;
+      if (!warp_wait_or_abort(&rec_full[rs], (j / ND) & 1, p.err, abort_flag, wl)) break;
       const TileRec& rec = recs[rs];
       if (rec.stop) break;
-      const bool full = rec.n == TT;
-      const int br = full ? rows : trows;
+      const bool whole = rec.n == TT;
+      const int br = whole ? rows : trows;
       const int nbox = (rec.n + br - 1) / br;
-      const int bytes = nbox * br * HD;
-      auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar) {
-        mbar_arrive_expect_tx_w(bar, bytes);
+      // lane b: the pool row of box b (counted from the first block's start)
+      const int r = lane * br + rec.row_in_blk;
+      int row = lane < nbox ? (rec.ids[r >> p.bs_log2] << p.bs_log2) + (r & (bs - 1)) : 0;
+      const int g = rec.item_g;
+      if (j >= NK && !warp_wait_or_abort(&empty[slot], ((j / NK) - 1) & 1, p.err, abort_flag, wl))
+        break;
+      mbar_arrive_expect_tx_w(&full[slot], nbox * br * HD);
+      const CUtensorMap* m = whole ? map : map_tail;
+      uint8_t* dst = ring + slot * kTileBytes;
 #pragma unroll 1
-        for (int b = 0; b < nbox; ++b) {
-          const int r = b * br + rec.row_in_blk;  // row counted from the first block's start
-          const int row = (rec.ids[r >> p.bs_log2] << p.bs_log2) + (r & (bs - 1));
-          tma_load_3d_w(dst + b * br * HD, map, bar, 0, rec.item_g, row);
-        }
-      };
-      const int ks = jk % NK, vs = jv % NV;
-      if (jk >= NK && !warp_wait_or_abort(&k_empty[ks], ((jk / NK) - 1) & 1, p.err, abort_flag, wl))
-        break;
-      load(full ? &tmK : &tmKt, smem + C::kOffK + ks * kTileBytes, &k_full[ks]);
-      ++jk;
-      if (jv >= NV && !warp_wait_or_abort(&v_empty[vs], ((jv / NV) - 1) & 1, p.err, abort_flag, wl))
-        break;
-      load(full ? &tmV : &tmVt, smem + C::kOffV + vs * kTileBytes, &v_full[vs]);
-      ++jv;
+      for (int b = 0; b < nbox; ++b)
+        tma_load_3d_w(dst + b * br * HD, m, &full[slot], 0, g, __shfl_sync(0xffffffffu, row, b));
       __syncwarp();
       if (lane == 0) mbar_arrive(&rec_empty[rs]);
+      ++j;
     }
     // Every copy this warp started must have landed before the CTA ends; per slot only its
     // last one can still be in flight.
     if (lane == 0) {
 #pragma unroll 1
-      for (unsigned t = jk > NK ? jk - NK : 0; t < jk; ++t)
-        mbar_wait(&k_full[t % NK], (t / NK) & 1, p.err);
-#pragma unroll 1
-      for (unsigned t = jv > NV ? jv - NV : 0; t < jv; ++t)
-        mbar_wait(&v_full[t % NV], (t / NV) & 1, p.err);
+      for (unsigned t = j > NK ? j - NK : 0; t < j; ++t)
+        mbar_wait(&full[t % NK], (t / NK) & 1, p.err);
     }
   } else if (warp == 14) {
     // ======================================================== scheduler
     unsigned j = 0;  // tile records published
     int k = 0;       // items
     bool alive = true;
-    // the sequence and head group of unit u0: walk the sequences 32 at a time
-    unsigned long long cum = 0;  // units before sequence s0
-    int s0 = 0;
-    int s = 0, hg = 0, nt = 0;
-    if (u0 < u1) {
-      while (true) {
-        const int t = tiles_of(s0 + lane);
-        int inc = t;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += up;
-        }
-        const int total = __shfl_sync(0xffffffffu, inc, 31);
-        if (cum + static_cast<unsigned long long>(total) * hgroups > u0) {
-          const unsigned hit = __ballot_sync(
-              0xffffffffu, cum + static_cast<unsigned long long>(inc) * hgroups > u0);
-          const int at = __ffs(hit) - 1;
-          nt = __shfl_sync(0xffffffffu, t, at);
-          const int before = __shfl_sync(0xffffffffu, inc - t, at);
-          cum += static_cast<unsigned long long>(before) * hgroups;
-          s = s0 + at;
-          break;
-        }
-        cum += static_cast<unsigned long long>(total) * hgroups;
-        s0 += 32;
-      }
-      hg = static_cast<int>((u0 - cum) / nt);
-      cum += static_cast<unsigned long long>(hg) * nt;  // units before (s, hg)
-    }
-    unsigned long long u = u0;
-    while (alive && u < u1) {
-      // item: the tiles of (s, hg) inside [u, u1)
-      const int ta = static_cast<int>(u - cum);
-      const unsigned long long end = cum + nt < u1 ? cum + nt : u1;
-      const int tb = static_cast<int>(end - cum);
-      const int g = hg * p.members + member;
-      int ctx = __ldg(p.context_lens + s);
-      if (ctx > p.max_context_len) {
-        if (lane == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
-        ctx = p.max_context_len;
-      }
-      // q first: its latency runs under the block ids'
+    int ta = first_tile;
+    unsigned run_at = run_end ? it_cum + ta * kTileCost : 0;
+    while (alive && run_at < run_end) {
+      // item: the tiles of (it_s, it_hg) from ta on that start before run_end
+      const int s = it_s, g = it_hg * p.members + member;
+      const int tiles = (it_ctx + TT - 1) / TT;
+      const int upto = static_cast<int>((run_end - it_cum + kTileCost - 1) / kTileCost);
+      const int tb = tiles < upto ? tiles : upto;
+      // q: its latency runs under the block ids'
       uint2 qraw[G];
       {
         const uint2* src = reinterpret_cast<const uint2*>(
@@ -464,20 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < G; ++h) qraw[h] = __ldg(src + h * (HD / 4) + lane);
       }
-      // parts of (s, hg): group i holds units [units i / groups, units (i + 1) / groups)
-      const unsigned long long ng = groups;
-      const int gf = static_cast<int>(((cum + 1) * ng - 1) / units);
-      const int gl = static_cast<int>(((cum + nt) * ng - 1) / units);
-      const int slot0 = units * gf / ng == cum ? 0 : 1;
-      const int part = group - gf;
-      const int which = part == 0 ? slot0 : 0;
-      const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks;
-      const int nblk = (ctx + bs - 1) >> p.bs_log2;
       const int per_tile = bs >= TT ? 1 : TT >> p.bs_log2;
       float ref = 0.f;
-      int bb = -32;  // first block of the batch of 32 held by the lanes
-      int id = 0;
       float ksc = 0.f, vsc = 0.f;
+      int scaled = -1;  // batch whose scales the lanes hold
       for (int t = ta; t < tb; ++t) {
         const int slot = j % ND;
         if (j >= ND &&
@@ -486,43 +516,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         TileRec& rec = recs[slot];
-        const int b0 = static_cast<int>((static_cast<int64_t>(t) * TT) >> p.bs_log2);
-        if (b0 >= bb + 32 || bb < 0) {
-          bb = b0;
-          const int b = bb + lane;
-          id = -1;
-          if (b < nblk && b < p.max_blocks) id = __ldg(table + b);
-          if (id < 0 || id >= p.num_blocks) {
-            if (b < nblk) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
-            id = 0;  // in-bounds stand-in
-          }
+        const int b0 = (t * TT) >> p.bs_log2;
+        if (b0 >= bb + 32) load_ids(b0);
+        if (scaled != bb && (bid < 0 || bid >= p.num_blocks)) {
+          if (((bb + lane) << p.bs_log2) < it_ctx) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+          bid = 0;  // in-bounds stand-in
         }
         const int l0 = b0 - bb;
         const bool mine = lane >= l0 && lane < l0 + per_tile;
-        if (mine) rec.ids[lane - l0] = id;
+        if (mine) rec.ids[lane - l0] = bid;
         if (lane == 0) {
-          rec.n = ctx - t * TT < TT ? ctx - t * TT : TT;
+          rec.n = it_ctx - t * TT < TT ? it_ctx - t * TT : TT;
           rec.first = t == ta;
           rec.last = t == tb - 1;
           rec.stop = 0;
           rec.row_in_blk = bs > TT ? (t * TT) & (bs - 1) : 0;
-          rec.item_s = s;
           rec.item_g = g;
-          rec.part = part;
-          rec.nparts = gl - gf + 1;
-          rec.group0 = gf;
-          rec.slot0 = slot0;
-          rec.which = which;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&rec_full[slot]);
         // the scales follow (the tile's loads do not wait for them)
-        if (b0 == bb) {
-          const int64_t at = static_cast<int64_t>(id) * p.num_kv_heads + g;
+        if (scaled != bb) {
+          scaled = bb;
+          const int64_t at = static_cast<int64_t>(bid) * p.num_kv_heads + g;
           ksc = __ldg(p.k_scales + at);
           vsc = __ldg(p.v_scales + at);
         }
-        const bool used = mine && b0 + (lane - l0) < nblk;
+        const bool used = mine && ((b0 + lane - l0) << p.bs_log2) < it_ctx;
         const float top = warp_max(used ? vsc : 0.f);
         const float now = fmaxf(ref, top);
         if (mine) {
@@ -530,6 +550,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           rec.vs[lane - l0] = now > 0.f ? __fdiv_rn(vsc, now) : 0.f;
         }
         if (lane == 0) {
+          if (t == tb - 1) {  // what the epilogue needs
+            const int group0 = group_of(it_cum);
+            rec.item_s = s;
+            rec.group0 = group0;
+            rec.part = group - group0;
+            rec.nparts = group_of(it_cum + (tiles - 1) * kTileCost) - group0 + 1;
+          }
           rec.ref = now;
           rec.alpha = (t == ta || now == ref || ref == 0.f) ? 1.f : __fdiv_rn(ref, now);
         }
@@ -575,15 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       ++k;
-      u = end;
-      // next (s, hg)
-      cum = cum + nt;
-      if (u < u1 && ++hg == hgroups) {
-        hg = 0;
-        do {
-          ++s;
-          nt = tiles_of(s);
-        } while (nt == 0 && s < p.num_seqs);
+      run_at = it_cum + it_cost;
+      if (run_at < run_end) {
+        pick(run_at);
+        load_ids(0);
+        ta = 0;
       }
     }
     if (alive) {
@@ -731,11 +754,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const TileRec& rec = recs[rs];
       const bool stop = rec.stop != 0;
       float x[G];
-      bool valid = false, first = false;
+      bool valid = false, first = false, exceeds = false;
       float vrel = 0.f;
-      float* rb = red + (j & 1) * 8 * G;
       // warp-uniform: the loads below are warp-wide
-      if (__all_sync(0xffffffffu, !failed && !stop)) {
+      const bool go = __all_sync(0xffffffffu, !failed && !stop);
+      if (go) {
         first = rec.first != 0;
         valid = pos < rec.n;
         failed |= !wait_or_abort(&scl_full[rs], (j / ND) & 1, p.err, abort_flag, wl);
@@ -755,52 +778,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[sb]);
+        exceeds = first;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float d = (sv[3 * h] + sv[3 * h + 1]) + sv[3 * h + 2];
           x[h] = valid ? d * (fs[h] * ksc) : -INFINITY;
-          const float v = warp_max(x[h]);
-          if (lane == 0) rb[h * 8 + warp] = v;
+          exceeds |= x[h] > m[h] + kBound;
         }
       }
-      if (bar_or(1, kSoftThreads, failed || stop)) {
-        if (tid == 0 && stop && !failed) {  // tell the epilogue there are no more items
-          const int b = k % NO;
-          if (k < NO || wait_or_abort(&epi_empty[b], ((k / NO) - 1) & 1, p.err, abort_flag, wl)) {
-            reinterpret_cast<ItemRec*>(smem + C::kOffEpi + b * C::kEpiBytes)->stop = 1;
-            mbar_arrive(&epi_full[b]);
+      // One vote a tile: nothing to do (the reference holds for every position), or the
+      // reference must move, or the loop ends.
+      float alpha[G], pp[G];
+      bool moved = false;
+      if (bar_or(1, kSoftThreads, failed || stop || exceeds)) {
+        float* rb = red + (j & 1) * 8 * G;
+        if (go) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float v = warp_max(x[h]);
+            if (lane == 0) rb[h * 8 + warp] = v;
           }
         }
-        break;
+        if (bar_or(1, kSoftThreads, failed || stop)) {
+          if (tid == 0 && stop && !failed) {  // tell the epilogue there are no more items
+            const int b = k % NO;
+            if (k < NO || wait_or_abort(&epi_empty[b], ((k / NO) - 1) & 1, p.err, abort_flag, wl)) {
+              reinterpret_cast<ItemRec*>(smem + C::kOffEpi + b * C::kEpiBytes)->stop = 1;
+              mbar_arrive(&epi_full[b]);
+            }
+          }
+          break;
+        }
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float4 w0 = *reinterpret_cast<const float4*>(rb + h * 8);
+          const float4 w1 = *reinterpret_cast<const float4*>(rb + h * 8 + 4);
+          const float mx = fmaxf(fmax3(fmaxf(w0.x, w0.y), w0.z, w0.w),
+                                 fmax3(fmaxf(w1.x, w1.y), w1.z, w1.w));
+          alpha[h] = 1.f;
+          if (first) {
+            m[h] = mx - kTarget;
+            l[h] = 0.f;
+          } else if (mx > m[h] + kBound) {
+            const float mn = mx - kTarget;
+            alpha[h] = ex2_approx(m[h] - mn);
+            l[h] *= alpha[h];
+            m[h] = mn;
+            moved = true;
+          }
+        }
       }
       // from here the record is known to be sound for every thread
       if (first && tid == 0) mbar_arrive(&q_empty[k % QN]);  // every thread has its q scales
       const int n = rec.n;
       const bool last = rec.last != 0;
       const float av = rec.alpha;
-      bool rescale = av != 1.f;
-      float alpha[G], pp[G];
+      bool rescale = moved || av != 1.f;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float4 w0 = *reinterpret_cast<const float4*>(rb + h * 8);
-        const float4 w1 = *reinterpret_cast<const float4*>(rb + h * 8 + 4);
-        const float mx = fmaxf(fmax3(fmaxf(w0.x, w0.y), w0.z, w0.w),
-                               fmax3(fmaxf(w1.x, w1.y), w1.z, w1.w));
-        alpha[h] = av;
-        if (first) {
-          m[h] = mx - kTarget;
-          l[h] = 0.f;
-        } else if (mx > m[h] + kBound) {
-          const float mn = mx - kTarget;
-          const float f = ex2_approx(m[h] - mn);
-          alpha[h] *= f;
-          l[h] *= f;
-          m[h] = mn;
-          rescale = true;
-        }
         const float e = valid ? ex2_approx(x[h] - m[h]) : 0.f;
         l[h] += e;
         pp[h] = e * vrel;
+        alpha[h] = moved ? alpha[h] * av : av;
       }
       if (first) rescale = false;  // O is overwritten by the item's first product
       // this P buffer was last read by the value product of tile j - NP
@@ -854,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       tc_fence_before();
       const float ref = rec.ref;
-      const ItemRec it{rec.item_s, rec.item_g, rec.part, rec.nparts, rec.group0, rec.slot0, rec.which, 0};
+      const ItemRec it{rec.item_s, rec.item_g, rec.part, rec.nparts, rec.group0, 0, {0, 0}};
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&p_full[pb]);
@@ -900,9 +939,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int dl = ((warp & 3) << 5) | lane;  // output dim = tensor-memory lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const bool leader = tid == 8 * 32;
-    // this CTA's four counters, tagged ahead of the arrivals
+    // this CTA's four counters get this call's tag ahead of the arrivals
     if (dl < 4) {
-      unsigned long long* ctr = p.counters + 2 * (blockIdx.x + (dl >> 1) * gridDim.x) + (dl & 1);
+      unsigned long long* ctr = p.counters + 4 * blockIdx.x + dl;
       tagged_install(ctr, *reinterpret_cast<volatile unsigned long long*>(ctr), p.tag, p.err);
     }
     // empty contexts: a zero row for every head
@@ -923,9 +962,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         L[h] = reinterpret_cast<const float*>(es + 32)[16 + h];
       }
       const float ref = reinterpret_cast<const float*>(es + 32)[32];
+      // part i of an item lives in CTA (group0 + i, member): a CTA's first item in slot 0 when
+      // it began in an earlier group, its last item in slot 1 when it goes on in a later one
+      auto slot_of = [&](int i) -> int64_t {
+        return 2 * (static_cast<int64_t>(it.group0 + i) * p.members + member) + (i == 0 ? 1 : 0);
+      };
+      // Are all the other parts there already (a CTA's last item, as a rule: the next CTA took
+      // its rest first)? Then they are merged while this one's last products run, and this
+      // part goes straight into the output.
+      if (leader && !failed && !it.stop && it.nparts > 1) {
+        unsigned long long v = 0;
+        if (it.nparts <= kFan) v = load_acquire(p.counters + 2 * slot_of(0));
+        *last_flag = v == ((p.tag << kCountBits) | static_cast<unsigned>(it.nparts - 1));
+      }
       if (bar_or(2, 128, failed)) break;  // every thread has read the hand-off
       if (leader) mbar_arrive(&epi_empty[b]);
       if (it.stop) break;
+      const bool finish = it.nparts > 1 && *last_flag != 0;
+      float om[G], ol[G], oo[G];  // the other parts
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        om[h] = -INFINITY;
+        ol[h] = 0.f;
+        oo[h] = 0.f;
+      }
+      if (finish) {
+#pragma unroll 1
+        for (int i = 0; i < it.nparts; ++i) {
+          if (i == it.part) continue;
+          const int64_t at = slot_of(i) * G;
+          float2 ml[G];
+          float po[G];
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            ml[h] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + at + h);
+            po[h] = __ldcg(p.ws_o + (at + h) * HD + dl);
+          }
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mx = fmaxf(om[h], ml[h].x);
+            const float r = ex2_approx(om[h] - mx), f = ex2_approx(ml[h].x - mx);
+            ol[h] = ol[h] * r + ml[h].y * f;
+            oo[h] = oo[h] * r + po[h] * f;
+            om[h] = mx;
+          }
+        }
+      }
       failed |= !wait_or_abort(&o_full[b], (k / NO) & 1, p.err, abort_flag, wl);
       tc_fence_after();
       constexpr int OC = load_cols(2 * G);
@@ -938,26 +1020,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[b]);
       const int64_t row0 = static_cast<int64_t>(it.s) * Hq + it.g * G;
-      if (it.nparts == 1) {
+      if (it.nparts == 1 || finish) {
+        if (finish) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mx = fmaxf(om[h], m[h]);
+            const float r = ex2_approx(om[h] - mx), f = ex2_approx(m[h] - mx);
+            L[h] = ol[h] * r + L[h] * f;
+            o[h] = oo[h] * r + o[h] * f;
+          }
+          if (leader) *reinterpret_cast<volatile unsigned long long*>(p.counters + 2 * slot_of(0)) = 0ull;
+        }
         if (!failed) {
 #pragma unroll
           for (int h = 0; h < G; ++h) p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(o[h] / L[h]);
         }
       } else {
-        // part i lives in slot 0 of CTA (group0 + i, member), the first one in slot0
-        auto slot_of = [&](int i) -> int64_t {
-          return 2 * (static_cast<int64_t>(it.group0 + i) * p.members + member) + (i == 0 ? it.slot0 : 0);
-        };
-        auto put_partial = [&](int64_t slot, int h, float pm, float pl, float po) {
-          p.ws_o[(slot * G + h) * HD + dl] = po;
-          if (dl == 0) *reinterpret_cast<float2*>(p.ws_ml + (slot * G + h) * 2) = make_float2(pm, pl);
-        };
-        const int64_t second = 2ll * gridDim.x;  // where the first level's results start
-        const int64_t mine = 2ll * blockIdx.x + it.which;
+        const int64_t mine = slot_of(it.part);
 #pragma unroll
-        for (int h = 0; h < G; ++h) put_partial(mine, h, m[h], L[h], o[h]);
-        auto put_out = [&](int h, float, float pl, float po) {
-          p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(po / pl);
+        for (int h = 0; h < G; ++h) {
+          p.ws_o[(mine * G + h) * HD + dl] = o[h];
+          if (dl == 0) *reinterpret_cast<float2*>(p.ws_ml + (mine * G + h) * 2) = make_float2(m[h], L[h]);
+        }
+        auto put_out = [&](int h, int dim, float, float pl, float4 a) {
+          *reinterpret_cast<uint2*>(p.out + (row0 + h) * HD + dim) =
+              make_uint2(pack_bf16x2(a.x / pl, a.y / pl), pack_bf16x2(a.z / pl, a.w / pl));
         };
         // arrive: written by all 128 threads, one release by the leader
         auto arrive = [&](unsigned long long* ctr, int total) -> bool {
@@ -976,18 +1063,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const int sub = it.part / kFan, nsub = (it.nparts + kFan - 1) / kFan;
         const int in_sub = it.nparts - sub * kFan < kFan ? it.nparts - sub * kFan : kFan;
-        bool top = nsub == 1;
-        const bool lead1 = arrive(p.counters + slot_of(sub * kFan), in_sub);
-        if (lead1) {
+        // arrivals of sixteen parts count at the first one's slot; when there are more parts,
+        // each sixteen's result replaces its first part, and those arrive at part 0's second
+        // counter
+        if (arrive(p.counters + 2 * slot_of(sub * kFan), in_sub)) {
           auto at = [&](int i) { return slot_of(sub * kFan + i); };
-          if (top) {
-            merge_parts<G>(p, in_sub, dl, at, put_out);
+          float* buf = reinterpret_cast<float*>(smem + C::kOffMerge);
+          if (nsub == 1) {
+            merge_parts<G>(p, in_sub, warp - 8, lane, buf, at, put_out);
           } else {
-            const int64_t to = second + slot_of(sub * kFan);
-            merge_parts<G>(p, in_sub, dl, at,
-                           [&](int h, float pm, float pl, float po) { put_partial(to, h, pm, pl, po); });
-            if (arrive(p.counters + second + slot_of(0), nsub))
-              merge_parts<G>(p, nsub, dl, [&](int i) { return second + slot_of(i * kFan); }, put_out);
+            const int64_t to = at(0);  // read and written by the same warps
+            merge_parts<G>(p, in_sub, warp - 8, lane, buf, at,
+                           [&](int h, int dim, float pm, float pl, float4 a) {
+                             *reinterpret_cast<float4*>(p.ws_o + (to * G + h) * HD + dim) = a;
+                             if (dim == 0)
+                               *reinterpret_cast<float2*>(p.ws_ml + (to * G + h) * 2) = make_float2(pm, pl);
+                           });
+            if (arrive(p.counters + 2 * slot_of(0) + 1, nsub))
+              merge_parts<G>(p, nsub, warp - 8, lane, buf,
+                             [&](int i) { return slot_of(i * kFan); }, put_out);
           }
         }
       }
@@ -1033,10 +1127,16 @@ cudaError_t launch_g(const DecodeLaunch& a, BsParams p, cudaStream_t stream) {
 
 }  // namespace
 
+// Slots of partials: two per CTA (its first and its last item); two counters per slot.
+namespace {
+size_t counter_bytes(size_t slots) { return (2 * slots * 8 + 255) / 256 * 256; }
+}  // namespace
+
 size_t decode_blockscale_workspace(int32_t num_q_heads, int32_t num_kv_heads) {
-  const size_t grid = static_cast<size_t>(sm_count());
-  const size_t g = static_cast<size_t>(num_q_heads / num_kv_heads);
-  return round_up(static_cast<int>(4 * grid * 8), 256) + 4 * grid * g * (HD + 2) * sizeof(float);
+  const int members = group_members(num_kv_heads);
+  const size_t slots = 2 * static_cast<size_t>(sm_count() / members * members);
+  return counter_bytes(slots) +
+         slots * static_cast<size_t>(num_q_heads / num_kv_heads) * (HD + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_blockscale(const DecodeLaunch& a, void* workspace, cudaStream_t stream) {
@@ -1057,6 +1157,7 @@ cudaError_t launch_decode_blockscale(const DecodeLaunch& a, void* workspace, cud
   const int64_t tiles = static_cast<int64_t>(a.num_seqs) *
                         (a.max_context_len > 0 ? (a.max_context_len + TT - 1) / TT : 1) *
                         (a.cache.num_kv_heads / p.members);
+  if (tiles * kTileCost > INT32_MAX) return cudaErrorInvalidValue;
   p.groups = sm_count() / p.members;
   if (p.groups < 1) return cudaErrorInvalidValue;
   if (tiles < p.groups) p.groups = static_cast<int>(tiles);
@@ -1066,11 +1167,10 @@ cudaError_t launch_decode_blockscale(const DecodeLaunch& a, void* workspace, cud
   p.max_context_len = a.max_context_len;
   p.scale_log2 = a.scale * kLog2eF;
   const int G = a.num_q_heads / a.cache.num_kv_heads;
-  const size_t grid = static_cast<size_t>(p.groups) * p.members;
+  const size_t slots = 2 * static_cast<size_t>(p.groups * p.members);
   p.counters = static_cast<unsigned long long*>(workspace);
-  p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                    round_up(static_cast<int>(4 * grid * 8), 256));
-  p.ws_ml = p.ws_o + 4 * grid * G * HD;
+  p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes(slots));
+  p.ws_ml = p.ws_o + slots * G * HD;
   switch (G) {
     case 1: return launch_g<1>(a, p, stream);
     case 2: return launch_g<2>(a, p, stream);
