@@ -32,7 +32,8 @@
 //
 // Bound: HBM (every K/V code is read once). Roles, as in the bf16 decode but streaming whole
 // runs: warps 0-7 softmax (two groups, one position of a 256-position tile per thread),
-// 8-11 epilogue, 12 and 15 TMA producers of K and of V, 13 tensor-core issuer, 14 scheduler.
+// 8-11 epilogue, 12 K (loads and score products), 13 V (loads and value products), 14
+// scheduler.
 // The scheduler publishes each tile's block ids and scales through a ring of tile records.
 //
 // Waits name an mbarrier phase by its parity, so a wait for phase n must know that phase
@@ -63,7 +64,7 @@ constexpr int NO = 2;          // O^T accumulators
 constexpr int kMaxBlk = 16;    // blocks of one tile (block size 16)
 constexpr int kTileBytes = TT * HD;
 constexpr int kHalf = TM * HD;
-constexpr int kThreads = 512;
+constexpr int kThreads = 480;
 constexpr int kSoftThreads = 256;
 constexpr int kFan = 16;       // parts merged at a time
 constexpr int kTileCost = 8;   // of a full tile, in units of 32 positions
@@ -121,7 +122,7 @@ struct Cfg {
   // heads shared by several epilogue warps meet here when parts are merged
   static constexpr int kOffMerge = round_up(kOffEpi + NO * kEpiBytes, 16);
   static constexpr int kOffBar = kOffMerge + (G < 4 ? 4 * (HD + 4) * 4 : 0);
-  static constexpr int kNumBars = 3 * ND + 2 * NK + 2 * NV + 2 * NS + 2 * NP + 2 * QN + 4 * NO + 1;
+  static constexpr int kNumBars = 3 * ND + 2 * NK + 2 * NV + 2 * NS + 2 * NP + 2 * QN + 4 * NO + 2;
   static constexpr int kOffMisc = round_up(kOffBar + 8 * kNumBars, 16);
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
   static constexpr uint32_t kSCols = 2 * NSR;  // two products of 128 positions
@@ -289,16 +290,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned long long wl = p.wait_ns;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* rec_full = bars;            // [ND] block ids of a tile -> producers, issuer, softmax
+  uint64_t* rec_full = bars;            // [ND] block ids of a tile -> K and V warps, softmax
   uint64_t* scl_full = rec_full + ND;   // [ND] its scales -> softmax
-  uint64_t* rec_empty = scl_full + ND;  // [ND] producers, issuer and softmax are done with it
-  uint64_t* k_full = rec_empty + ND;    // [NK] TMA -> issuer
-  uint64_t* k_empty = k_full + NK;      // [NK] score product done -> producer
-  uint64_t* v_full = k_empty + NK;      // [NV] TMA -> issuer (+ softmax on a last tile)
-  uint64_t* v_empty = v_full + NV;      // [NV] value product done -> producer
+  uint64_t* rec_empty = scl_full + ND;  // [ND] K and V warps and softmax are done with it
+  uint64_t* k_full = rec_empty + ND;    // [NK] K landed
+  uint64_t* k_empty = k_full + NK;      // [NK] score product done
+  uint64_t* v_full = k_empty + NK;      // [NV] V landed (also the softmax's on a last tile)
+  uint64_t* v_empty = v_full + NV;      // [NV] value product done
   uint64_t* s_full = v_empty + NV;      // [NS] score product done -> softmax
   uint64_t* s_free = s_full + NS;       // [NS] softmax has read S
-  uint64_t* p_full = s_free + NS;       // [NP] P written -> issuer
+  uint64_t* p_full = s_free + NS;       // [NP] P written -> V warp
   uint64_t* pv_done = p_full + NP;      // [NP] value product done -> softmax
   uint64_t* q_ready = pv_done + NP;     // [QN] q terms and scales written
   uint64_t* q_empty = q_ready + QN;     // [QN] score products of the item done, scales read
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_free = o_full + NO;       // [NO] epilogue has read O
   uint64_t* epi_full = o_free + NO;     // [NO] softmax hand-off
   uint64_t* epi_empty = epi_full + NO;  // [NO] epilogue has read it
-  uint64_t* mma_drain = epi_empty + NO;
+  uint64_t* mma_drain = epi_empty + NO;  // [2] every product of the K / V warp has finished
   TileRec* recs = reinterpret_cast<TileRec*>(smem + C::kOffRec);
   float* red = reinterpret_cast<float*>(smem + C::kOffRed);
   float* qscale = reinterpret_cast<float*>(smem + C::kOffQs);  // [QN][G]
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < C::kNumBars) {
     uint64_t* bar = bars + tid;
     auto in = [&](uint64_t* first, int n) { return bar >= first && bar < first + n; };
-    const unsigned count = in(rec_empty, ND)                      ? 3 + kSoftThreads / 32
+    const unsigned count = in(rec_empty, ND)                      ? 2 + kSoftThreads / 32
                            : in(s_free, NS) || in(p_full, NP)     ? kSoftThreads / 32
                            : in(q_empty, QN)                      ? 2
                            : in(o_free, NO)                       ? 4
@@ -438,51 +439,156 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 12 || warp == 15) {
-    // ======================================================== TMA producers (K: 12, V: 15)
-    const bool is_v = warp == 15;
+  if (warp == 12 || warp == 13) {
+    // ======================================================== K warp (12) and V warp (13)
+    // Each loads its tiles into its ring and issues the products that read them: an event loop
+    // over a load cursor and a product cursor, loads first. (One warp issuing both products,
+    // beside two loading ones, took 2400 of a tile's 2860 cycles and held the rings full.)
+    const bool is_v = warp == 13;
     const CUtensorMap* map = is_v ? &tmV : &tmK;
     const CUtensorMap* map_tail = is_v ? &tmVt : &tmKt;
     uint8_t* ring = smem + (is_v ? C::kOffV : C::kOffK);
     uint64_t* full = is_v ? v_full : k_full;
     uint64_t* empty = is_v ? v_empty : k_empty;
     static_assert(NK == NV, "one ring depth");
+    constexpr uint32_t idS = idesc_e4m3_f32(TM, NSR, 0, 0);  // K K-major, q terms K-major
+    constexpr uint32_t idO = idesc_e4m3_f32(HD, NPR, 1, 0);  // V^T MN-major, P terms K-major
+    const uint64_t ring_desc = smem_desc_sw128(smem_u32(ring), is_v ? kHalf : 16, 1024);
+    const uint64_t b_desc = smem_desc_sw128(smem_u32(smem + (is_v ? C::kOffP : C::kOffQ)), 16, 1024);
     if (lane == 0) prefetch_tensormap(map);
     __syncwarp();
-    const int rows = bs < TT ? bs : TT;    // rows per box of a full tile
-    const int trows = bs < 32 ? bs : 32;   // of a context's last tile (no rows past it)
-    unsigned j = 0;  // tiles whose loads were started
-    while (true) {
-      const int rs = j % ND, slot = j % NK;
-      if (!warp_wait_or_abort(&rec_full[rs], (j / ND) & 1, p.err, abort_flag, wl)) break;
+    const int rows = bs < TT ? bs : TT;   // rows per box of a full tile
+    const int trows = bs < 32 ? bs : 32;  // of a context's last tile (no rows past it)
+    unsigned jl = 0, jm = 0;              // tiles whose load / product was issued
+    int item = 0;                         // of the product cursor
+    bool ended = false;                   // the stop record was seen
+    // load of tile jl (false: no record yet, or no free slot)
+    auto load = [&]() -> bool {
+      const int rs = jl % ND, slot = jl % NK;
+      if (!__all_sync(0xffffffffu,
+                      mbar_test_wait(&rec_full[rs], (jl / ND) & 1) &&
+                          (jl < NK || mbar_test_wait(&empty[slot], ((jl / NK) - 1) & 1))))
+        return false;
       const TileRec& rec = recs[rs];
-      if (rec.stop) break;
+      if (rec.stop) {
+        ended = true;
+        return false;
+      }
       const bool whole = rec.n == TT;
       const int br = whole ? rows : trows;
       const int nbox = (rec.n + br - 1) / br;
       // lane b: the pool row of box b (counted from the first block's start)
       const int r = lane * br + rec.row_in_blk;
-      int row = lane < nbox ? (rec.ids[r >> p.bs_log2] << p.bs_log2) + (r & (bs - 1)) : 0;
+      const int row = lane < nbox ? (rec.ids[r >> p.bs_log2] << p.bs_log2) + (r & (bs - 1)) : 0;
       const int g = rec.item_g;
-      if (j >= NK && !warp_wait_or_abort(&empty[slot], ((j / NK) - 1) & 1, p.err, abort_flag, wl))
-        break;
-      mbar_arrive_expect_tx_w(&full[slot], nbox * br * HD);
       const CUtensorMap* m = whole ? map : map_tail;
       uint8_t* dst = ring + slot * kTileBytes;
+      mbar_arrive_expect_tx_w(&full[slot], nbox * br * HD);
 #pragma unroll 1
       for (int b = 0; b < nbox; ++b)
         tma_load_3d_w(dst + b * br * HD, m, &full[slot], 0, g, __shfl_sync(0xffffffffu, row, b));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rec_empty[rs]);
-      ++j;
+      ++jl;
+      return true;
+    };
+    // S of tile jm (false: its q, K tile or S buffer is not ready)
+    auto score = [&]() -> bool {
+      const int slot = jm % NK, sb = jm % NS, qs = item % QN;
+      const TileRec& rec = recs[jm % ND];
+      if (!__all_sync(0xffffffffu,
+                      mbar_test_wait(&k_full[slot], (jm / NK) & 1) &&
+                          (jm < NS || mbar_test_wait(&s_free[sb], ((jm / NS) - 1) & 1)) &&
+                          (!rec.first || mbar_test_wait(&q_ready[qs], (item / QN) & 1))))
+        return false;
+      tc_fence_after();
+      const uint64_t aK = desc_advance(ring_desc, slot * kTileBytes);
+      const uint64_t bQ = desc_advance(b_desc, qs * C::kQBytes);
+      const uint32_t dS = tmem + sb * C::kSCols;
+#pragma unroll
+      for (int kk = 0; kk < HD / 32; ++kk)
+        tc_mma_f8_ss(dS, desc_advance(aK, kk * 32), desc_advance(bQ, kk * 32), idS, kk > 0 ? 1u : 0u);
+      if (rec.n > TM) {
+#pragma unroll
+        for (int kk = 0; kk < HD / 32; ++kk)
+          tc_mma_f8_ss(dS + NSR, desc_advance(aK, kHalf + kk * 32), desc_advance(bQ, kk * 32), idS,
+                       kk > 0 ? 1u : 0u);
+      }
+      tc_commit(&s_full[sb]);
+      tc_commit(&k_empty[slot]);
+      if (rec.last) {
+        tc_commit(&q_empty[qs]);
+        ++item;
+      }
+      return true;
+    };
+    // O += V^T P^T of tile jm (false: P, V or the accumulator is not ready)
+    auto value = [&]() -> bool {
+      const int pb = jm % NP, slot = jm % NV, ob = item % NO;
+      const TileRec& rec = recs[jm % ND];
+      const bool first = rec.first != 0;
+      if (!__all_sync(0xffffffffu,
+                      mbar_test_wait(&p_full[pb], (jm / NP) & 1) &&
+                          mbar_test_wait(&v_full[slot], (jm / NV) & 1) &&
+                          (!first || item < NO || mbar_test_wait(&o_free[ob], ((item / NO) - 1) & 1))))
+        return false;
+      tc_fence_after();
+      const uint64_t aV = desc_advance(ring_desc, slot * kTileBytes);
+      const uint64_t bP = desc_advance(b_desc, pb * C::kPBytes);
+      const uint32_t dO = tmem + C::kTmemO + ob * NPR;
+      const int steps = (rec.n + 31) >> 5;  // 32 positions each; none past the context
+#pragma unroll
+      for (int kk = 0; kk < TT / 32; ++kk)
+        if (kk < steps)
+          tc_mma_f8_ss(dO, desc_advance(aV, kk * 32 * 128),
+                       desc_advance(bP, (kk >> 2) * C::kPChunk + (kk & 3) * 32), idO,
+                       (first && kk == 0) ? 0u : 1u);
+      tc_commit(&pv_done[pb]);
+      tc_commit(&v_empty[slot]);
+      if (rec.last) {
+        tc_commit(&o_full[ob]);
+        ++item;
+      }
+      return true;
+    };
+    unsigned long long idle_since = 0;
+    while (true) {
+      bool progressed = !ended && load();
+      if (jm < jl && (is_v ? value() : score())) {
+        if (lane == 0) mbar_arrive(&rec_empty[jm % ND]);
+        ++jm;
+        progressed = true;
+      }
+      if (ended && jm == jl) break;
+      if (progressed) {
+        idle_since = 0;
+        continue;
+      }
+      if (jm == jl)
+        mbar_try_wait(&rec_full[jl % ND], (jl / ND) & 1);
+      else if (is_v)
+        mbar_try_wait(&p_full[jm % NP], (jm / NP) & 1);
+      else
+        mbar_try_wait(&k_full[jm % NK], (jm / NK) & 1);
+      const unsigned long long now = globaltimer_ns();
+      if (idle_since == 0) idle_since = now;
+      const bool give_up = *abort_flag || now - idle_since > wl;
+      if (__any_sync(0xffffffffu, give_up)) {
+        if (!*abort_flag) {
+          if (lane == 0) flag_error(p.err, PA_DEV_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        break;
+      }
     }
-    // Every copy this warp started must have landed before the CTA ends; per slot only its
-    // last one can still be in flight.
+    // Before the CTA ends: every copy this warp started has landed (per slot only its last one
+    // can still be in flight), every product it issued has finished.
     if (lane == 0) {
 #pragma unroll 1
-      for (unsigned t = j > NK ? j - NK : 0; t < j; ++t)
+      for (unsigned t = jl > NK ? jl - NK : 0; t < jl; ++t)
         mbar_wait(&full[t % NK], (t / NK) & 1, p.err);
     }
+    __syncwarp();
+    tc_commit(&mma_drain[is_v]);
+    mbar_wait(&mma_drain[is_v], 0, p.err);
   } else if (warp == 14) {
     // ======================================================== scheduler
     unsigned j = 0;  // tile records published
@@ -620,111 +726,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 13) {
-    // ======================================================== tensor-core issuer
-    constexpr uint32_t idS = idesc_e4m3_f32(TM, NSR, 0, 0);  // K K-major, q terms K-major
-    constexpr uint32_t idO = idesc_e4m3_f32(HD, NPR, 1, 0);  // V^T MN-major, P terms K-major
-    const uint32_t sP = smem_u32(smem + C::kOffP);
-    unsigned js = 0, jp = 0;  // score and value cursors (tiles)
-    int ks = 0, kp = 0;       // their items
-    bool s_end = false;
-    // S of tile js (false: its record, q, K tile or S buffer is not ready)
-    auto score = [&]() -> bool {
-      if (s_end) return false;
-      const int rs = js % ND;
-      if (!__all_sync(0xffffffffu, mbar_test_wait(&rec_full[rs], (js / ND) & 1))) return false;
-      const TileRec& rec = recs[rs];
-      if (rec.stop) {
-        s_end = true;
-        return false;
-      }
-      const int kslot = js % NK, sb = js % NS, qs = ks % QN;
-      if (!__all_sync(0xffffffffu,
-                      mbar_test_wait(&k_full[kslot], (js / NK) & 1) &&
-                          (js < NS || mbar_test_wait(&s_free[sb], ((js / NS) - 1) & 1)) &&
-                          (!rec.first || mbar_test_wait(&q_ready[qs], (ks / QN) & 1))))
-        return false;
-      tc_fence_after();
-      const uint64_t aK = smem_desc_sw128(smem_u32(smem + C::kOffK + kslot * kTileBytes), 16, 1024);
-      const uint64_t bQ = smem_desc_sw128(smem_u32(smem + C::kOffQ + qs * C::kQBytes), 16, 1024);
-      const uint32_t dS = tmem + sb * C::kSCols;
-#pragma unroll
-      for (int kk = 0; kk < HD / 32; ++kk)
-        tc_mma_f8_ss(dS, desc_advance(aK, kk * 32), desc_advance(bQ, kk * 32), idS, kk > 0 ? 1u : 0u);
-      if (rec.n > TM) {
-#pragma unroll
-        for (int kk = 0; kk < HD / 32; ++kk)
-          tc_mma_f8_ss(dS + NSR, desc_advance(aK, kHalf + kk * 32), desc_advance(bQ, kk * 32), idS,
-                       kk > 0 ? 1u : 0u);
-      }
-      tc_commit(&s_full[sb]);
-      tc_commit(&k_empty[kslot]);
-      if (rec.last) {
-        tc_commit(&q_empty[qs]);
-        ++ks;
-      }
-      ++js;
-      return true;
-    };
-    // O += V^T P^T of tile jp (false: P, V or the accumulator is not ready)
-    auto value = [&]() -> bool {
-      const int pb = jp % NP, vs = jp % NV, ob = kp % NO;
-      const TileRec& rec = recs[jp % ND];
-      const bool first = rec.first != 0;
-      if (!__all_sync(0xffffffffu,
-                      mbar_test_wait(&p_full[pb], (jp / NP) & 1) &&
-                          mbar_test_wait(&v_full[vs], (jp / NV) & 1) &&
-                          (!first || kp < NO || mbar_test_wait(&o_free[ob], ((kp / NO) - 1) & 1))))
-        return false;
-      tc_fence_after();
-      const uint64_t aV = smem_desc_sw128(smem_u32(smem + C::kOffV + vs * kTileBytes), kHalf, 1024);
-      const uint64_t bP = smem_desc_sw128(sP + pb * C::kPBytes, 16, 1024);
-      const uint32_t dO = tmem + C::kTmemO + ob * NPR;
-      const int steps = (rec.n + 31) >> 5;  // 32 positions each; none past the context
-#pragma unroll
-      for (int kk = 0; kk < TT / 32; ++kk)
-        if (kk < steps)
-          tc_mma_f8_ss(dO, desc_advance(aV, kk * 32 * 128),
-                       desc_advance(bP, (kk >> 2) * C::kPChunk + (kk & 3) * 32), idO,
-                       (first && kk == 0) ? 0u : 1u);
-      tc_commit(&pv_done[pb]);
-      tc_commit(&v_empty[vs]);
-      if (rec.last) {
-        tc_commit(&o_full[ob]);
-        ++kp;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rec_empty[jp % ND]);
-      ++jp;
-      return true;
-    };
-    unsigned long long idle_since = 0;
-    while (true) {
-      // a value product first: the softmax and the V ring wait on it
-      const bool progressed = (jp < js && value()) || (js < jp + NS && score());
-      if (jp == js && s_end) break;
-      if (progressed) {
-        idle_since = 0;
-        continue;
-      }
-      if (jp < js)
-        mbar_try_wait(&p_full[jp % NP], (jp / NP) & 1);
-      else
-        mbar_try_wait(&k_full[js % NK], (js / NK) & 1);
-      const unsigned long long now = globaltimer_ns();
-      if (idle_since == 0) idle_since = now;
-      const bool give_up = *abort_flag || now - idle_since > wl;
-      if (__any_sync(0xffffffffu, give_up)) {
-        if (!*abort_flag) {
-          if (lane == 0) flag_error(p.err, PA_DEV_ERR_TIMEOUT);
-          *abort_flag = 1;
-        }
-        break;
-      }
-    }
-    // every product has finished before tensor and shared memory go away
-    tc_commit(mma_drain);
-    mbar_wait(mma_drain, 0, p.err);
   } else if (warp < 8) {
     // ======================================================== softmax
     // Thread r of group sg owns position 128 sg + r of each tile. Control flow is uniform
