@@ -554,7 +554,8 @@ pa_status pa_rope_store_kvcache_fp8_blockscale(
  *                   captured into a CUDA graph replays as it is (its counters are left
  *                   ready; only after a call that timed out must the workspace be cleared
  *                   before such a replay).
- * Supported: head_dim 128, Hq / Hkv in {1, 2, 4, 8, 16}; else PA_ERR_UNSUPPORTED.
+ * Supported: head_dim 128, Hq / Hkv in {1, 2, 4, 8, 16}, max_context_len up to 2^30 and
+ * num_seqs * Hkv * (max_context_len / 32 + 16) below 2^31; else PA_ERR_UNSUPPORTED.
  */
 size_t pa_decode_fp8_blockscale_workspace_size(int32_t num_q_heads, int32_t num_kv_heads);
 pa_status pa_decode_fp8_blockscale(void* out, const void* q, const void* k_codes,

@@ -33,7 +33,7 @@
 // Bound: HBM (every K/V code is read once). Roles, as in the bf16 decode but streaming whole
 // runs: warps 0-7 softmax (two groups, one position of a 256-position tile per thread),
 // 8-11 epilogue, 12 K (loads and score products), 13 V (loads and value products), 14
-// scheduler.
+// scheduler, 15 q terms.
 // The scheduler publishes each tile's block ids and scales through a ring of tile records.
 //
 // Waits name an mbarrier phase by its parity, so a wait for phase n must know that phase
@@ -64,7 +64,7 @@ constexpr int NO = 2;          // O^T accumulators
 constexpr int kMaxBlk = 16;    // blocks of one tile (block size 16)
 constexpr int kTileBytes = TT * HD;
 constexpr int kHalf = TM * HD;
-constexpr int kThreads = 480;
+constexpr int kThreads = 512;
 constexpr int kSoftThreads = 256;
 constexpr int kFan = 16;       // parts merged at a time
 constexpr int kTileCost = 8;   // of a full tile, in units of 32 positions
@@ -290,9 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned long long wl = p.wait_ns;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* rec_full = bars;            // [ND] block ids of a tile -> K and V warps, softmax
+  uint64_t* rec_full = bars;            // [ND] a tile's place -> K, V and q warps, softmax
   uint64_t* scl_full = rec_full + ND;   // [ND] its scales -> softmax
-  uint64_t* rec_empty = scl_full + ND;  // [ND] K and V warps and softmax are done with it
+  uint64_t* rec_empty = scl_full + ND;  // [ND] K, V and q warps and softmax are done with it
   uint64_t* k_full = rec_empty + ND;    // [NK] K landed
   uint64_t* k_empty = k_full + NK;      // [NK] score product done
   uint64_t* v_full = k_empty + NK;      // [NV] V landed (also the softmax's on a last tile)
@@ -349,22 +349,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     wtotal = __shfl_sync(0xffffffffu, winc, 31) * hgroups;
   };
-  // the current item: sequence, head group, context, its cost and the cost before it
-  int it_s = 0, it_hg = 0, it_ctx = 0;
-  unsigned it_cost = 0, it_cum = 0;
-  auto pick = [&](unsigned c) {  // the item that holds cost c
+  // an item: sequence, head group, context, its cost and the cost before it
+  struct Item {
+    int s, hg, ctx;
+    unsigned cost, cum;
+  };
+  auto pick = [&](unsigned c) -> Item {  // the item that holds cost c
     while (wbase + wtotal <= c) {
       wbase += wtotal;
       seq0 += 32;
       window();
     }
     const int at = __ffs(__ballot_sync(0xffffffffu, wbase + winc * hgroups > c)) - 1;
-    it_cost = __shfl_sync(0xffffffffu, wcost, at);
-    it_ctx = __shfl_sync(0xffffffffu, wctx, at);
-    const unsigned before = wbase + (__shfl_sync(0xffffffffu, winc, at) - it_cost) * hgroups;
-    it_s = seq0 + at;
-    it_hg = static_cast<int>((c - before) / it_cost);
-    it_cum = before + it_hg * it_cost;
+    Item it;
+    it.cost = __shfl_sync(0xffffffffu, wcost, at);
+    it.ctx = __shfl_sync(0xffffffffu, wctx, at);
+    const unsigned before = wbase + (__shfl_sync(0xffffffffu, winc, at) - it.cost) * hgroups;
+    it.s = seq0 + at;
+    it.hg = static_cast<int>((c - before) / it.cost);
+    it.cum = before + it.hg * it.cost;
+    return it;
   };
   // group i takes the tiles that start in [run_start(i), run_start(i + 1))
   unsigned cost = 0, run_q = 0, run_r = 0;
@@ -373,19 +377,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned wide = run_r * (run_q + 1);
     return c < wide ? c / (run_q + 1) : run_r + (c - wide) / run_q;
   };
-  // block ids of 32 blocks from bb on
-  int bb = 0, bid = 0;
-  auto load_ids = [&](int b0) {
-    bb = b0;
+  // block ids of an item's 32 blocks from b0 on, one per lane
+  auto load_ids = [&](const Item& it, int b0) -> int {
     const int b = b0 + lane;
-    bid = -1;
-    if ((b << p.bs_log2) < it_ctx && b < p.max_blocks)
-      bid = __ldg(p.block_tables + static_cast<int64_t>(it_s) * p.max_blocks + b);
+    return (b << p.bs_log2) < it.ctx && b < p.max_blocks
+               ? __ldg(p.block_tables + static_cast<int64_t>(it.s) * p.max_blocks + b)
+               : -1;
   };
   // The scheduler counts the costs and reads its first block ids before the set-up barrier,
   // so that these dependent reads overlap the set-up.
   unsigned run_end = 0;
-  int first_tile = 0;
+  Item next{};         // the scheduler's next item, with its first tile, first block and ids
+  int next_ta = 0, next_bb = 0, next_ids = -1;
   if (warp == 14) {
     window();
     cost = wtotal;
@@ -403,14 +406,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       run_r = cost - run_q * groups;
       const unsigned start = run_start(group);
       run_end = run_start(group + 1);
-      pick(start);
-      first_tile = static_cast<int>((start - it_cum + kTileCost - 1) / kTileCost);
-      if (first_tile * TT >= it_ctx) {  // the run starts inside the item's last tile
-        first_tile = 0;
-        if (it_cum + it_cost < run_end) pick(it_cum + it_cost);
+      next = pick(start);
+      next_ta = static_cast<int>((start - next.cum + kTileCost - 1) / kTileCost);
+      if (next_ta * TT >= next.ctx) {  // the run starts inside the item's last tile
+        next_ta = 0;
+        if (next.cum + next.cost < run_end) next = pick(next.cum + next.cost);
         else run_end = 0;
       }
-      if (run_end) load_ids((first_tile * TT) >> p.bs_log2);
+      if (run_end) {
+        next_bb = (next_ta * TT) >> p.bs_log2;
+        next_ids = load_ids(next, next_bb);
+      }
     }
   }
 
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < C::kNumBars) {
     uint64_t* bar = bars + tid;
     auto in = [&](uint64_t* first, int n) { return bar >= first && bar < first + n; };
-    const unsigned count = in(rec_empty, ND)                      ? 2 + kSoftThreads / 32
+    const unsigned count = in(rec_empty, ND)                      ? 3 + kSoftThreads / 32
                            : in(s_free, NS) || in(p_full, NP)     ? kSoftThreads / 32
                            : in(q_empty, QN)                      ? 2
                            : in(o_free, NO)                       ? 4
@@ -457,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t b_desc = smem_desc_sw128(smem_u32(smem + (is_v ? C::kOffP : C::kOffQ)), 16, 1024);
     if (lane == 0) prefetch_tensormap(map);
     __syncwarp();
-    const int rows = bs < TT ? bs : TT;   // rows per box of a full tile
-    const int trows = bs < 32 ? bs : 32;  // of a context's last tile (no rows past it)
+    const int rows_log2 = bs < TT ? p.bs_log2 : 8;   // rows per box of a full tile
+    const int trows_log2 = bs < 32 ? p.bs_log2 : 5;  // of a context's last tile (none past it)
     unsigned jl = 0, jm = 0;              // tiles whose load / product was issued
     int item = 0;                         // of the product cursor
     bool ended = false;                   // the stop record was seen
@@ -475,18 +481,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
       }
       const bool whole = rec.n == TT;
-      const int br = whole ? rows : trows;
-      const int nbox = (rec.n + br - 1) / br;
+      const int br_log2 = whole ? rows_log2 : trows_log2;
+      const int nbox = (rec.n + (1 << br_log2) - 1) >> br_log2;
       // lane b: the pool row of box b (counted from the first block's start)
-      const int r = lane * br + rec.row_in_blk;
+      const int r = (lane << br_log2) + rec.row_in_blk;
       const int row = lane < nbox ? (rec.ids[r >> p.bs_log2] << p.bs_log2) + (r & (bs - 1)) : 0;
       const int g = rec.item_g;
       const CUtensorMap* m = whole ? map : map_tail;
       uint8_t* dst = ring + slot * kTileBytes;
-      mbar_arrive_expect_tx_w(&full[slot], nbox * br * HD);
+      mbar_arrive_expect_tx_w(&full[slot], (nbox << br_log2) * HD);
 #pragma unroll 1
       for (int b = 0; b < nbox; ++b)
-        tma_load_3d_w(dst + b * br * HD, m, &full[slot], 0, g, __shfl_sync(0xffffffffu, row, b));
+        tma_load_3d_w(dst + ((b << br_log2) * HD), m, &full[slot], 0, g,
+                      __shfl_sync(0xffffffffu, row, b));
       ++jl;
       return true;
     };
@@ -550,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     unsigned long long idle_since = 0;
+    unsigned idle = 0;
     while (true) {
       bool progressed = !ended && load();
       if (jm < jl && (is_v ? value() : score())) {
@@ -559,17 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ended && jm == jl) break;
       if (progressed) {
-        idle_since = 0;
+        idle = 0;
         continue;
       }
-      if (jm == jl)
-        mbar_try_wait(&rec_full[jl % ND], (jl / ND) & 1);
-      else if (is_v)
-        mbar_try_wait(&p_full[jm % NP], (jm / NP) & 1);
-      else
-        mbar_try_wait(&k_full[jm % NK], (jm / NK) & 1);
+      if ((++idle & 3) != 1) continue;  // polls; the timer is read at the first and then now and then
       const unsigned long long now = globaltimer_ns();
-      if (idle_since == 0) idle_since = now;
+      if (idle == 1) idle_since = now;
       const bool give_up = *abort_flag || now - idle_since > wl;
       if (__any_sync(0xffffffffu, give_up)) {
         if (!*abort_flag) {
@@ -592,28 +595,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 14) {
     // ======================================================== scheduler
     unsigned j = 0;  // tile records published
-    int k = 0;       // items
     bool alive = true;
-    int ta = first_tile;
-    unsigned run_at = run_end ? it_cum + ta * kTileCost : 0;
-    while (alive && run_at < run_end) {
-      // item: the tiles of (it_s, it_hg) from ta on that start before run_end
-      const int s = it_s, g = it_hg * p.members + member;
-      const int tiles = (it_ctx + TT - 1) / TT;
-      const int upto = static_cast<int>((run_end - it_cum + kTileCost - 1) / kTileCost);
+    const int per_tile = bs >= TT ? 1 : TT >> p.bs_log2;
+    bool more = run_end > 0;
+    while (alive && more) {
+      // item: its tiles from ta on that start before run_end
+      const Item it = next;
+      const int ta = next_ta;
+      int bb = next_bb, bid = next_ids;  // first block and ids of the batch the lanes hold
+      const int g = it.hg * p.members + member;
+      const int tiles = (it.ctx + TT - 1) / TT;
+      const int upto = static_cast<int>((run_end - it.cum + kTileCost - 1) / kTileCost);
       const int tb = tiles < upto ? tiles : upto;
-      // q: its latency runs under the block ids'
-      uint2 qraw[G];
-      {
-        const uint2* src = reinterpret_cast<const uint2*>(
-            p.q + (static_cast<int64_t>(s) * Hq + g * G) * HD);
-#pragma unroll
-        for (int h = 0; h < G; ++h) qraw[h] = __ldg(src + h * (HD / 4) + lane);
+      // the next item's ids are on their way while this one's tiles are published
+      more = it.cum + it.cost < run_end;
+      if (more) {
+        next = pick(it.cum + it.cost);
+        next_ta = next_bb = 0;
+        next_ids = load_ids(next, 0);
       }
-      const int per_tile = bs >= TT ? 1 : TT >> p.bs_log2;
       float ref = 0.f;
       float ksc = 0.f, vsc = 0.f;
-      int scaled = -1;  // batch whose scales the lanes hold
+      bool fresh = true;  // the batch's scales have not been read
       for (int t = ta; t < tb; ++t) {
         const int slot = j % ND;
         if (j >= ND &&
@@ -623,96 +626,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         TileRec& rec = recs[slot];
         const int b0 = (t * TT) >> p.bs_log2;
-        if (b0 >= bb + 32) load_ids(b0);
-        if (scaled != bb && (bid < 0 || bid >= p.num_blocks)) {
-          if (((bb + lane) << p.bs_log2) < it_ctx) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+        if (b0 >= bb + 32) {
+          bb = b0;
+          bid = load_ids(it, b0);
+          fresh = true;
+        }
+        if (fresh && (bid < 0 || bid >= p.num_blocks)) {
+          if (((bb + lane) << p.bs_log2) < it.ctx) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
           bid = 0;  // in-bounds stand-in
         }
         const int l0 = b0 - bb;
         const bool mine = lane >= l0 && lane < l0 + per_tile;
         if (mine) rec.ids[lane - l0] = bid;
         if (lane == 0) {
-          rec.n = it_ctx - t * TT < TT ? it_ctx - t * TT : TT;
+          rec.n = it.ctx - t * TT < TT ? it.ctx - t * TT : TT;
           rec.first = t == ta;
           rec.last = t == tb - 1;
           rec.stop = 0;
           rec.row_in_blk = bs > TT ? (t * TT) & (bs - 1) : 0;
+          rec.item_s = it.s;
           rec.item_g = g;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&rec_full[slot]);
         // the scales follow (the tile's loads do not wait for them)
-        if (scaled != bb) {
-          scaled = bb;
+        if (fresh) {
+          fresh = false;
           const int64_t at = static_cast<int64_t>(bid) * p.num_kv_heads + g;
           ksc = __ldg(p.k_scales + at);
           vsc = __ldg(p.v_scales + at);
         }
-        const bool used = mine && ((b0 + lane - l0) << p.bs_log2) < it_ctx;
-        const float top = warp_max(used ? vsc : 0.f);
-        const float now = fmaxf(ref, top);
+        const bool used = mine && ((b0 + lane - l0) << p.bs_log2) < it.ctx;
+        const float now = fmaxf(ref, warp_max(used ? vsc : 0.f));
         if (mine) {
           rec.ks[lane - l0] = ksc;
-          rec.vs[lane - l0] = now > 0.f ? __fdiv_rn(vsc, now) : 0.f;
+          rec.vs[lane - l0] = now > 0.f ? __fdividef(vsc, now) : 0.f;
         }
         if (lane == 0) {
           if (t == tb - 1) {  // what the epilogue needs
-            const int group0 = group_of(it_cum);
-            rec.item_s = s;
+            const int group0 = group_of(it.cum);
             rec.group0 = group0;
             rec.part = group - group0;
-            rec.nparts = group_of(it_cum + (tiles - 1) * kTileCost) - group0 + 1;
+            rec.nparts = group_of(it.cum + (tiles - 1) * kTileCost) - group0 + 1;
           }
           rec.ref = now;
-          rec.alpha = (t == ta || now == ref || ref == 0.f) ? 1.f : __fdiv_rn(ref, now);
+          rec.alpha = (t == ta || now == ref || ref == 0.f) ? 1.f : __fdividef(ref, now);
         }
         ref = now;
         __syncwarp();
         if (lane == 0) mbar_arrive(&scl_full[slot]);
         ++j;
-        if (t == ta) {
-          // q terms of the item: lane L holds dims 4L .. 4L + 3
-          const int qs = k % QN;
-          if (k >= QN &&
-              !warp_wait_or_abort(&q_empty[qs], ((k / QN) - 1) & 1, p.err, abort_flag, wl)) {
-            alive = false;
-            break;
-          }
-          uint8_t* qd = smem + C::kOffQ + qs * C::kQBytes;
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float f0 = bf16lo_to_f32(qraw[h].x), f1 = bf16hi_to_f32(qraw[h].x);
-            const float f2 = bf16lo_to_f32(qraw[h].y), f3 = bf16hi_to_f32(qraw[h].y);
-            const float amax = warp_max(fmaxf(fmaxf(fabsf(f0), fabsf(f1)), fmaxf(fabsf(f2), fabsf(f3))));
-            float inv = 448.f / amax;
-            if (!(inv <= FLT_MAX)) inv = 0.f;  // all zero (or tiny): codes 0, scale 0
-            float y[4] = {f0 * inv, f1 * inv, f2 * inv, f3 * inv};
-#pragma unroll
-            for (int term = 0; term < 3; ++term) {
-              const int row = 3 * h + term;
-              float2 b01, b23;
-              const uint32_t c01 = e4m3x2(y[0], y[1], b01);
-              const uint32_t c23 = e4m3x2(y[2], y[3], b23);
-              *reinterpret_cast<uint32_t*>(qd + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
-                                           (lane & 3) * 4) = c01 | (c23 << 16);
-              y[0] -= b01.x;
-              y[1] -= b01.y;
-              y[2] -= b23.x;
-              y[3] -= b23.y;
-            }
-            if (lane == 0) qscale[qs * G + h] = inv > 0.f ? amax / 448.f : 0.f;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&q_ready[qs]);
-        }
-      }
-      ++k;
-      run_at = it_cum + it_cost;
-      if (run_at < run_end) {
-        pick(run_at);
-        load_ids(0);
-        ta = 0;
       }
     }
     if (alive) {
@@ -725,6 +688,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&rec_full[slot]);
         }
       }
+    }
+  } else if (warp == 15) {
+    // ======================================================== q warp
+    // The q terms of every item, from its first tile's record on: lane L holds dims 4L .. 4L + 3.
+    int k = 0;
+    for (unsigned j = 0;; ++j) {
+      const int rs = j % ND;
+      if (!warp_wait_or_abort(&rec_full[rs], (j / ND) & 1, p.err, abort_flag, wl)) break;
+      const TileRec& rec = recs[rs];
+      if (rec.stop) break;
+      if (rec.first) {
+        const uint2* src = reinterpret_cast<const uint2*>(
+            p.q + (static_cast<int64_t>(rec.item_s) * Hq + rec.item_g * G) * HD);
+        uint2 raw[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) raw[h] = __ldg(src + h * (HD / 4) + lane);
+        const int qs = k % QN;
+        if (k >= QN &&
+            !warp_wait_or_abort(&q_empty[qs], ((k / QN) - 1) & 1, p.err, abort_flag, wl))
+          break;
+        uint8_t* qd = smem + C::kOffQ + qs * C::kQBytes;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float f0 = bf16lo_to_f32(raw[h].x), f1 = bf16hi_to_f32(raw[h].x);
+          const float f2 = bf16lo_to_f32(raw[h].y), f3 = bf16hi_to_f32(raw[h].y);
+          const float amax = warp_max(fmaxf(fmaxf(fabsf(f0), fabsf(f1)), fmaxf(fabsf(f2), fabsf(f3))));
+          float inv = 448.f / amax;
+          if (!(inv <= FLT_MAX)) inv = 0.f;  // all zero (or tiny): codes 0, scale 0
+          float y[4] = {f0 * inv, f1 * inv, f2 * inv, f3 * inv};
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            const int row = 3 * h + term;
+            float2 b01, b23;
+            const uint32_t c01 = e4m3x2(y[0], y[1], b01);
+            const uint32_t c23 = e4m3x2(y[2], y[3], b23);
+            *reinterpret_cast<uint32_t*>(qd + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
+                                         (lane & 3) * 4) = c01 | (c23 << 16);
+            y[0] -= b01.x;
+            y[1] -= b01.y;
+            y[2] -= b23.x;
+            y[3] -= b23.y;
+          }
+          if (lane == 0) qscale[qs * G + h] = inv > 0.f ? amax / 448.f : 0.f;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_ready[qs]);
+        ++k;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rec_empty[rs]);
     }
   } else if (warp < 8) {
     // ======================================================== softmax
@@ -1158,7 +1172,6 @@ cudaError_t launch_decode_blockscale(const DecodeLaunch& a, void* workspace, cud
   const int64_t tiles = static_cast<int64_t>(a.num_seqs) *
                         (a.max_context_len > 0 ? (a.max_context_len + TT - 1) / TT : 1) *
                         (a.cache.num_kv_heads / p.members);
-  if (tiles * kTileCost > INT32_MAX) return cudaErrorInvalidValue;
   p.groups = sm_count() / p.members;
   if (p.groups < 1) return cudaErrorInvalidValue;
   if (tiles < p.groups) p.groups = static_cast<int>(tiles);

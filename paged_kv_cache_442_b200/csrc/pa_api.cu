@@ -711,6 +711,10 @@ pa_status pa_decode_fp8_blockscale(void* out, const void* q, const void* k_codes
   const int G = num_q_heads / cache.num_kv_heads;
   if (cache.head_dim != 128 || (G != 1 && G != 2 && G != 4 && G != 8 && G != 16))
     return PA_ERR_UNSUPPORTED;
+  // the split counts the batch in 32-position steps of every (sequence, kv head), in 32 bits
+  if (max_context_len > (1 << 30) ||
+      (static_cast<int64_t>(max_context_len) / 32 + 16) * num_seqs >= INT32_MAX / cache.num_kv_heads)
+    return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   if (!out || !q || !k_codes || !v_codes || !k_scales || !v_scales || !block_tables || !context_lens)
     return PA_ERR_INVALID_ARG;
