@@ -201,32 +201,36 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float (&v)[N]) {
   else tmem_st32(taddr, v);
 }
 
-// One merge step over cnt <= kFan parts, part i at slot_of(i), by the four epilogue warps: a
-// warp takes whole heads (G >= 4) or a head's parts in turn with 4 / G - 1 other warps. Lane i
-// reads part i's maximum and sum; the lanes hold 4 output dims each, so a part's row is one
-// 16-byte load per lane, and all of a head's loads are in flight together. Reads bypass L1
-// (the parts were written by other SMs). put(h, dim, M, L, A): head h, dims dim .. dim + 3.
-template <int G, class SlotOf, class Put>
-__device__ __forceinline__ void merge_parts(const BsParams& p, int cnt, int warp4, int lane,
-                                            float* buf, SlotOf slot_of, Put put) {
+// One merge step over cnt <= kFan parts by the four epilogue warps; part i's record is at slot
+// first + i * step, but part 0's at `slot0`. A warp takes whole heads (G >= 4) or a head's
+// parts in turn with 4 / G - 1 other warps. Lane i reads part i's maximum and sum; the lanes
+// hold 4 output dims each, so a part's row is one 16-byte load per lane, and all of a head's
+// loads are in flight together. Reads bypass L1 (the parts were written by other SMs).
+// out non-NULL: the rows' outputs; NULL: the result replaces part 0's record (read and written
+// by the same warps).
+template <int G>
+__device__ __forceinline__ void merge_parts(float* ws_o, float* ws_ml, int cnt, int slot0, int first,
+                                         int step, int warp4, int lane, float* buf,
+                                         __nv_bfloat16* out) {
   constexpr int S = G >= 4 ? 1 : 4 / G;  // warps that share a head
   constexpr int N = kFan / S;            // parts of one warp
   const int sub = G >= 4 ? 0 : warp4 / G;
+  auto slot_of = [&](int i) -> int64_t { return i == 0 ? slot0 : first + i * step; };
 #pragma unroll 1
   for (int h = G >= 4 ? warp4 : warp4 % G; h < G; h += 4) {
     const int part = lane * S + sub;  // lane i holds the warp's i-th part
     const bool in = lane < N && part < cnt;
-    const float2 ml = in ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot_of(part) * G + h)
+    const float2 ml = in ? __ldcg(reinterpret_cast<const float2*>(ws_ml) + slot_of(part) * G + h)
                          : make_float2(-INFINITY, 0.f);
     float4 o[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i * S + sub < cnt)
-        o[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (slot_of(i * S + sub) * G + h) * HD) + lane);
+        o[i] = __ldcg(reinterpret_cast<const float4*>(ws_o + (slot_of(i * S + sub) * G + h) * HD) + lane);
     }
     float M = warp_max(ml.x);
-    float f = M > -INFINITY ? ex2_approx(ml.x - M) : 0.f;
+    const float f = M > -INFINITY ? ex2_approx(ml.x - M) : 0.f;
     float L = ml.y * f;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
@@ -267,7 +271,17 @@ __device__ __forceinline__ void merge_parts(const BsParams& p, int cnt, int warp
       }
       named_bar_sync(2, 128);  // before the buffer's next use
     }
-    if (sub == 0) put(h, 4 * lane, M, L, A);
+    if (sub == 0) {
+      if (out) {
+        const float r = __fdividef(1.f, L);
+        *reinterpret_cast<uint2*>(out + h * HD + 4 * lane) =
+            make_uint2(pack_bf16x2(A.x * r, A.y * r), pack_bf16x2(A.z * r, A.w * r));
+      } else {
+        const int64_t to = static_cast<int64_t>(slot0) * G + h;
+        reinterpret_cast<float4*>(ws_o + to * HD)[lane] = A;
+        if (lane == 0) *reinterpret_cast<float2*>(ws_ml + to * 2) = make_float2(M, L);
+      }
+    }
   }
 }
 
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cost = wtotal;
     if (p.num_seqs > 32) {
       unsigned sum = 0;
-#pragma unroll 2
+#pragma unroll 1
       for (int s = 32 + lane; s < p.num_seqs; s += 32) sum += cost_of(context(s));
       cost += __reduce_add_sync(0xffffffffu, sum) * hgroups;
     }
@@ -406,12 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       run_r = cost - run_q * groups;
       const unsigned start = run_start(group);
       run_end = run_start(group + 1);
-      next = pick(start);
-      next_ta = static_cast<int>((start - next.cum + kTileCost - 1) / kTileCost);
-      if (next_ta * TT >= next.ctx) {  // the run starts inside the item's last tile
-        next_ta = 0;
-        if (next.cum + next.cost < run_end) next = pick(next.cum + next.cost);
-        else run_end = 0;
+      unsigned c = start;
+#pragma unroll 1
+      while (true) {
+        next = pick(c);
+        next_ta = c == start ? static_cast<int>((start - next.cum + kTileCost - 1) / kTileCost) : 0;
+        if (next_ta * TT < next.ctx) break;
+        c = next.cum + next.cost;  // the run starts inside the item's last tile
+        if (c >= run_end) {
+          run_end = 0;
+          break;
+        }
       }
       if (run_end) {
         next_bb = (next_ta * TT) >> p.bs_log2;
@@ -421,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // q slots and P buffers start at zero: rows that no head uses stay zero
+#pragma unroll 1
   for (int i = tid; i < (QN * C::kQBytes + NP * C::kPBytes) / 16; i += kThreads)
     reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
@@ -960,8 +980,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tagged_install(ctr, *reinterpret_cast<volatile unsigned long long*>(ctr), p.tag, p.err);
     }
     // empty contexts: a zero row for every head
+#pragma unroll 1
     for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
       if (__ldg(p.context_lens + s) <= 0)
+#pragma unroll 1
         for (int i = dl; i < Hq * HD / 2; i += 128)
           reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(s) * Hq * HD)[i] = 0u;
     int k = 0;
@@ -1048,7 +1070,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!failed) {
 #pragma unroll
-          for (int h = 0; h < G; ++h) p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(o[h] / L[h]);
+          for (int h = 0; h < G; ++h)
+            p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(__fdividef(o[h], L[h]));
         }
       } else {
         const int64_t mine = slot_of(it.part);
@@ -1057,10 +1080,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.ws_o[(mine * G + h) * HD + dl] = o[h];
           if (dl == 0) *reinterpret_cast<float2*>(p.ws_ml + (mine * G + h) * 2) = make_float2(m[h], L[h]);
         }
-        auto put_out = [&](int h, int dim, float, float pl, float4 a) {
-          *reinterpret_cast<uint2*>(p.out + (row0 + h) * HD + dim) =
-              make_uint2(pack_bf16x2(a.x / pl, a.y / pl), pack_bf16x2(a.z / pl, a.w / pl));
-        };
         // arrive: written by all 128 threads, one release by the leader
         auto arrive = [&](unsigned long long* ctr, int total) -> bool {
           named_bar_sync(2, 128);
@@ -1081,23 +1100,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // arrivals of sixteen parts count at the first one's slot; when there are more parts,
         // each sixteen's result replaces its first part, and those arrive at part 0's second
         // counter
-        if (arrive(p.counters + 2 * slot_of(sub * kFan), in_sub)) {
-          auto at = [&](int i) { return slot_of(sub * kFan + i); };
-          float* buf = reinterpret_cast<float*>(smem + C::kOffMerge);
-          if (nsub == 1) {
-            merge_parts<G>(p, in_sub, warp - 8, lane, buf, at, put_out);
-          } else {
-            const int64_t to = at(0);  // read and written by the same warps
-            merge_parts<G>(p, in_sub, warp - 8, lane, buf, at,
-                           [&](int h, int dim, float pm, float pl, float4 a) {
-                             *reinterpret_cast<float4*>(p.ws_o + (to * G + h) * HD + dim) = a;
-                             if (dim == 0)
-                               *reinterpret_cast<float2*>(p.ws_ml + (to * G + h) * 2) = make_float2(pm, pl);
-                           });
-            if (arrive(p.counters + 2 * slot_of(0) + 1, nsub))
-              merge_parts<G>(p, nsub, warp - 8, lane, buf,
-                             [&](int i) { return slot_of(i * kFan); }, put_out);
-          }
+        const int base = static_cast<int>(slot_of(0)) - 1, per = 2 * p.members;  // of part 0 in slot 0
+        int from = sub * kFan, step = 1, cnt = in_sub;
+        bool top = nsub == 1;
+        unsigned long long* ctr = p.counters + 2 * slot_of(from);
+#pragma unroll 1
+        while (arrive(ctr, cnt)) {
+          merge_parts<G>(p.ws_o, p.ws_ml, cnt, static_cast<int>(slot_of(from)), base + from * per,
+                         step * per, warp - 8, lane, reinterpret_cast<float*>(smem + C::kOffMerge),
+                         top ? p.out + row0 * HD : nullptr);
+          if (top) break;
+          top = true;
+          from = 0;
+          step = kFan;
+          cnt = nsub;
+          ctr = p.counters + 2 * slot_of(0) + 1;
         }
       }
       if (bar_or(2, 128, failed)) break;  // also orders last_flag's reuse
