@@ -23,7 +23,8 @@
 // several heads (128 bytes each) are fetched together (one head per group: 82 us against
 // 59.5 on batch 64). All tiles, ordered by (sequence, head group, position), are cut into
 // runs of equal cost, one per group: a tile costs 8, a context's last tile as many eighths as
-// it has positions (4 at least). So a CTA takes at most two partial (sequence, kv head) items,
+// it has positions (4 at least), every item 5 more (fitted to the CTAs' times; without the 5,
+// 256 ragged contexts took 105 us instead of 100). So a CTA takes at most two partial items,
 // its first and its last, and every CTA knows how many parts an item is in; the CTA that
 // completes the last part merges them, sixteen parts at a time. (A share of the tiles left in
 // short chunks for the CTAs that are done first gained nothing: batch 64 59.6 - 61.5 us with
@@ -68,6 +69,8 @@ constexpr int kThreads = 512;
 constexpr int kSoftThreads = 256;
 constexpr int kFan = 16;       // parts merged at a time
 constexpr int kTileCost = 8;   // of a full tile, in units of 32 positions
+constexpr int kTailCost = 4;   // least of a context's last tile
+constexpr int kItemCost = 5;   // an item's own (its q terms, first reference and epilogue)
 constexpr float kTarget = 3.f;  // a new reference puts the largest P' at 2^kTarget ...
 constexpr float kBound = 6.f;   // ... and it moves when one would pass 2^kBound (128 (P' - hi)
                                 // is then at most 256, inside e4m3's 448)
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ctx == 0) return 0;
     const int tiles = (ctx + TT - 1) / TT;
     const int tail = (ctx - (tiles - 1) * TT + 31) / 32;
-    return static_cast<unsigned>((tiles - 1) * kTileCost + (tail > kTileCost / 2 ? tail : kTileCost / 2));
+    return static_cast<unsigned>((tiles - 1) * kTileCost + (tail > kTailCost ? tail : kTailCost) + kItemCost);
   };
   auto window = [&]() {
     wctx = context(seq0 + lane);
