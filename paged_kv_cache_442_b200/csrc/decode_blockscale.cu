@@ -171,6 +171,10 @@ __device__ __forceinline__ unsigned long long load_acquire(const unsigned long l
   return v;
 }
 
+__device__ __forceinline__ void fence_acq_rel_gpu() {
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");
+}
+
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -407,12 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item next{};         // the scheduler's next item, with its first tile, first block and ids
   int next_ta = 0, next_bb = 0, next_ids = -1;
   if (warp == 14) {
+    const int second = context(32 + lane);  // read beside the window's
     window();
     cost = wtotal;
     if (p.num_seqs > 32) {
-      unsigned sum = 0;
+      unsigned sum = cost_of(second);
 #pragma unroll 1
-      for (int s = 32 + lane; s < p.num_seqs; s += 32) sum += cost_of(context(s));
+      for (int s = 64 + lane; s < p.num_seqs; s += 32) sum += cost_of(context(s));
       cost += __reduce_add_sync(0xffffffffu, sum) * hgroups;
     }
     // runs at least a tile long: no run is skipped between two tiles of an item
@@ -630,13 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tiles = (it.ctx + TT - 1) / TT;
       const int upto = static_cast<int>((run_end - it.cum + kTileCost - 1) / kTileCost);
       const int tb = tiles < upto ? tiles : upto;
-      // the next item's ids are on their way while this one's tiles are published
       more = it.cum + it.cost < run_end;
-      if (more) {
-        next = pick(it.cum + it.cost);
-        next_ta = next_bb = 0;
-        next_ids = load_ids(next, 0);
-      }
       float ref = 0.f;
       float ksc = 0.f, vsc = 0.f;
       bool fresh = true;  // the batch's scales have not been read
@@ -699,6 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&scl_full[slot]);
         ++j;
+        // the next item's ids are on their way while this one's other tiles are published
+        if (t == ta && more) {
+          next = pick(it.cum + it.cost);
+          next_ta = next_bb = 0;
+          next_ids = load_ids(next, 0);
+        }
       }
     }
     if (alive) {
@@ -1087,13 +1092,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto arrive = [&](unsigned long long* ctr, int total) -> bool {
           named_bar_sync(2, 128);
           if (leader) {
-            __threadfence();
+            fence_acq_rel_gpu();
             bool okc = true;
             const unsigned before = tagged_arrive_many(ctr, p.tag, p.err, &okc);
             const bool is_last = okc && before == static_cast<unsigned>(total - 1);
             if (is_last) *reinterpret_cast<volatile unsigned long long*>(ctr) = 0ull;
             *last_flag = is_last;
-            __threadfence();
+            fence_acq_rel_gpu();
           }
           named_bar_sync(2, 128);
           return *last_flag != 0;
