@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeStorePar
   };
   load(hl);
 
-  table.fill(tid, kThreads, t0, p.num_tokens, p.positions, p.rope);
+  table.fill_tokens(tid, kThreads, t0, p.num_tokens, p.positions, p.rope);
   __syncthreads();
   const bool in_rot = g < (p.rope.rot_dim >> 4);
   const RopeTurns cs = table.group(tk, in_rot ? g : 0);

@@ -40,11 +40,10 @@ __device__ __forceinline__ unsigned long long rope_rate(float freq) {
          static_cast<unsigned long long>(__double2ll_rn(err * kTurn));
 }
 
-// cos and sin of 2 pi * (pos * rate), times the amplitude. The product's top 32 bits are the
-// angle to 2^-32 of a turn; its nearest quarter turn is split off, the rest (at most pi / 4)
-// goes through the Taylor series of sine (to x^9, next term below 2^-29) and cosine (to
-// x^10, next below 2^-33).
-__device__ __forceinline__ float2 rope_turn(int pos, unsigned long long rate, float amplitude) {
+// cos and sin of 2 pi * (pos * rate). The product's top 32 bits are the angle to 2^-32 of a
+// turn; its nearest quarter turn is split off, the rest (at most pi / 4) goes through the
+// Taylor series of sine (to x^9, next term below 2^-29) and cosine (to x^10, next below 2^-33).
+__device__ __forceinline__ float2 rope_circle(int pos, unsigned long long rate) {
   const unsigned long long t = static_cast<unsigned long long>(static_cast<long long>(pos)) * rate;
   const unsigned h = static_cast<unsigned>(t >> 32);
   const unsigned quarter = (h + 0x20000000u) >> 30;
@@ -64,8 +63,26 @@ __device__ __forceinline__ float2 rope_turn(int pos, unsigned long long rate, fl
   const bool odd = quarter & 1u;
   const float cc = odd ? s : c, ss = odd ? c : s;
   const unsigned cneg = ((quarter + 1u) & 2u) << 30, sneg = (quarter & 2u) << 30;
-  return make_float2(amplitude * __uint_as_float(__float_as_uint(cc) ^ cneg),
-                     amplitude * __uint_as_float(__float_as_uint(ss) ^ sneg));
+  return make_float2(__uint_as_float(__float_as_uint(cc) ^ cneg),
+                     __uint_as_float(__float_as_uint(ss) ^ sneg));
+}
+
+// The turn of a position is the product of two: of the position with its low four bits
+// cleared, times the amplitude, and of those four bits. Kernels that turn the same frequency
+// at many neighbouring positions keep both factors in tables (a 28-instruction series becomes
+// a packed product); every kernel computes the product in this order, so all agree bit for
+// bit. Two roundings more, each 2^-24.
+constexpr int kRopeLow = 16;
+__device__ __forceinline__ float2 rope_high(int pos, unsigned long long rate, float amplitude) {
+  const float2 t = rope_circle(pos & ~(kRopeLow - 1), rate);
+  return make_float2(amplitude * t.x, amplitude * t.y);
+}
+__device__ __forceinline__ float2 rope_low(int pos, unsigned long long rate) {
+  return rope_circle(pos & (kRopeLow - 1), rate);
+}
+__device__ __forceinline__ float2 rope_turn(int pos, unsigned long long rate, float amplitude) {
+  const float2 a = rope_high(pos, rate, amplitude), b = rope_low(pos, rate);
+  return make_float2(fmaf(a.y, -b.y, a.x * b.x), fmaf(a.y, b.x, a.x * b.y));
 }
 
 // One pair, in fp32, rounded once to bf16 by the caller. Every path computes it in this order
@@ -121,31 +138,31 @@ __device__ __forceinline__ int2 rope_vectors(int g, const RopeParams& r) {
   return (g < ng && !r.interleaved) ? make_int2(g, g + ng) : make_int2(2 * g, 2 * g + 1);
 }
 
-// Turns of TB tokens in shared memory, cosines and sines apart: the 8 of a group are two
-// 16-byte loads each, free of bank conflicts.
-template <int TB, int HALF>
-struct RopeTable {
-  alignas(16) float c[TB][HALF];
-  alignas(16) float s[TB][HALF];
+// Where frequency f of HALF sits in a row of a table: the first four of every group of eight,
+// then the second four, so that the eight threads of a head read a group's 16-byte halves
+// from consecutive addresses (no bank conflicts).
+template <int HALF>
+__device__ __forceinline__ int rope_place(int f) {
+  return ((f >> 2) & 1) * (HALF / 2) + (f >> 3) * 4 + (f & 3);
+}
 
-  __device__ __forceinline__ void fill(int tid, int threads, int64_t t0, int num_tokens,
-                                       const int32_t* positions, const RopeParams& r) {
-    const int half = r.rot_dim >> 1;
-    for (int i = tid; i < TB * half; i += threads) {
-      const int tt = i / half, f = i - tt * half;
-      if (t0 + tt >= num_tokens) break;
-      const float2 cs = rope_turn(__ldg(positions + t0 + tt), rope_rate(__ldg(r.inv_freq + f)),
-                                  r.amplitude);
-      c[tt][f] = cs.x;
-      s[tt][f] = cs.y;
-    }
+// A table of ROWS rows of cosines and sines (apart) in shared memory.
+template <int ROWS, int HALF>
+struct RopeTable {
+  alignas(16) float c[ROWS][HALF];
+  alignas(16) float s[ROWS][HALF];
+
+  __device__ __forceinline__ void put(int row, int f, float2 t) {
+    c[row][rope_place<HALF>(f)] = t.x;
+    s[row][rope_place<HALF>(f)] = t.y;
   }
-  __device__ __forceinline__ RopeTurns group(int tt, int g) const {
+  // the eight frequencies of group g
+  __device__ __forceinline__ RopeTurns group(int row, int g) const {
     RopeTurns t;
-    const float4 c0 = *reinterpret_cast<const float4*>(&c[tt][8 * g]);
-    const float4 c1 = *reinterpret_cast<const float4*>(&c[tt][8 * g + 4]);
-    const float4 s0 = *reinterpret_cast<const float4*>(&s[tt][8 * g]);
-    const float4 s1 = *reinterpret_cast<const float4*>(&s[tt][8 * g + 4]);
+    const float4 c0 = *reinterpret_cast<const float4*>(&c[row][4 * g]);
+    const float4 c1 = *reinterpret_cast<const float4*>(&c[row][HALF / 2 + 4 * g]);
+    const float4 s0 = *reinterpret_cast<const float4*>(&s[row][4 * g]);
+    const float4 s1 = *reinterpret_cast<const float4*>(&s[row][HALF / 2 + 4 * g]);
     t.c[0] = make_float2(c0.x, c0.y);
     t.c[1] = make_float2(c0.z, c0.w);
     t.c[2] = make_float2(c1.x, c1.y);
@@ -156,6 +173,30 @@ struct RopeTable {
     t.s[3] = make_float2(s1.z, s1.w);
     return t;
   }
+  // row i: the turns of token t0 + i
+  __device__ __forceinline__ void fill_tokens(int tid, int threads, int64_t t0, int num_tokens,
+                                              const int32_t* positions, const RopeParams& r) {
+    const int half = r.rot_dim >> 1;
+    if (half == 0) return;
+    // one frequency per thread, rows `step` apart
+    const int step = threads / half, row0 = tid / half, f = tid - row0 * half;
+    if (row0 >= step) return;
+    const unsigned long long rate = rope_rate(__ldg(r.inv_freq + f));
+    for (int row = row0; row < ROWS && t0 + row < num_tokens; row += step)
+      put(row, f, rope_turn(__ldg(positions + t0 + row), rate, r.amplitude));
+  }
 };
+
+// Products of two groups' turns, as rope_turn forms them.
+__device__ __forceinline__ RopeTurns rope_product(const RopeTurns& a, const RopeTurns& b) {
+  RopeTurns t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 nb = make_float2(-b.s[i].x, -b.s[i].y);
+    t.c[i] = __ffma2_rn(a.s[i], nb, __fmul2_rn(a.c[i], b.c[i]));
+    t.s[i] = __ffma2_rn(a.s[i], b.c[i], __fmul2_rn(a.c[i], b.s[i]));
+  }
+  return t;
+}
 
 }  // namespace pa

@@ -8,14 +8,12 @@
 // scale grow, the stored codes move by an exact power of two: only codes that fall into
 // e4m3's subnormal range are rounded again.
 //
-// Work: one unit per (sequence, block its new rows reach, K or V, kv head); a unit of W
-// warps loads its new rows (16 dims per thread and row: two 16-byte loads) into registers,
-// turns them (K), takes the largest finite magnitude on the bf16 bits, agrees on the scale
-// and writes the codes; rows already in the block are rewritten only when the scale grew.
-// No unit shares a (block, head) with another, so there are no atomics and the result does
-// not depend on the order. HBM-bound: a bf16 row in, half of it out. Blocks of up to 256
-// rows (512 at head dim 64) stay in registers between the two steps; larger ones are read
-// twice (the second time from L2).
+// Work: one unit per (sequence, block its new rows reach, K or V, kv head or heads), 16 dims
+// per thread and row (two 16-byte loads). A unit loads its new rows into registers, turns them
+// (K), takes the largest finite magnitude on the bf16 bits, agrees on the scale and writes the
+// codes; rows already in the block are rewritten only when the scale grew. No unit shares a
+// (block, head) with another, so there are no atomics and the result does not depend on the
+// order. HBM-bound: a bf16 row in, half of it out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -34,7 +32,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kFewRows = 32;    // new rows of a block that one warp takes
 constexpr int kRowHeads = 8;    // (row, head) pairs a thread keeps in registers (64 registers)
-constexpr int kMaxCluster = 8;  // portable cluster size
+constexpr int kMaxCluster = 4;  // CTAs that share a block of 1024 rows
 constexpr int kQTokens = 2;        // tokens of a CTA that turns queries
 
 struct AppendParams {
@@ -132,13 +130,6 @@ __device__ __forceinline__ void requantise_rows(uint8_t* codes, int64_t row_byte
   }
 }
 
-// The table's memory as rates of the frequencies (D / 2 of them) in CTAs without queries.
-template <int D2>
-__device__ __forceinline__ unsigned long long* rates_of(RopeTable<kQTokens, D2>& table) {
-  static_assert(sizeof(table) >= D2 * sizeof(unsigned long long), "rates fit the table");
-  return reinterpret_cast<unsigned long long*>(&table);
-}
-
 // The queries of kQTokens tokens (as in rope.cu).
 template <int D>
 __device__ __forceinline__ void turn_queries(const AppendParams& p,
@@ -165,7 +156,7 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p,
     }
   };
   load(hl);
-  table.fill(tid, kThreads, t0, p.num_tokens, p.positions, p.rope);
+  table.fill_tokens(tid, kThreads, t0, p.num_tokens, p.positions, p.rope);
   __syncthreads();
   const bool in_rot = g < (p.rope.rot_dim >> 4);
   const RopeTurns cs = table.group(tk, in_rot ? g : 0);
@@ -322,22 +313,34 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams
     requantise_rows<D>(codes, row_bytes, u.r0, __fdiv_rn(old, scale), lane, 32);
 }
 
-// Many new rows per block: a cluster of CTAs per (sequence, block, K or V, HT heads). A CTA
-// takes kRowHeads / HT rows per thread of the block, each in HT heads, so that the turns of a
-// (row, frequency) are computed once for HT heads, and a row's HT heads (256 bytes each) are
-// read together. The CTAs of a cluster hold one block between them and exchange their largest
-// magnitudes through distributed shared memory before they quantise.
+// Many new rows per block. A CTA takes RL * kRowHeads / HT rows of HT heads (64 rows of 4
+// heads, 128 of 2 or 256 of one at 128 dims), all in registers between the scan for the
+// largest magnitude and the quantising; a block with more rows is shared by a cluster of CTAs,
+// which exchange their largest magnitudes through distributed shared memory. HT is the
+// largest that holds a block's rows in one CTA: the turns of a row are then formed once for
+// HT heads, and a row's HT heads (256 bytes each) are read together. (Clusters of 64 rows of
+// 4 heads for blocks of 256 measured 37.5 us without turns against 25 for one CTA of 256 rows
+// of one head, 16384 tokens of 8 kv heads: a cluster waits for its slowest load.)
+// Turns: two tables in shared memory, the high and the low factor (rope.cuh) of the CTA's
+// consecutive positions; a row whose position does not follow is turned by the series.
 template <int D, int HT>
 __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendParams p) {
   constexpr int NG = D / 16;
   constexpr int RL = kThreads / NG;      // rows side by side
   constexpr int RT = kRowHeads / HT;     // rows per thread
   constexpr int CAP = RL * RT;           // rows of a CTA
-  __shared__ RopeTable<kQTokens, D / 2> table;
+  constexpr int HIGH = CAP / kRopeLow + 1;
+  __shared__ union {
+    RopeTable<kQTokens, D / 2> queries;
+    struct {
+      RopeTable<HIGH, D / 2> high;
+      RopeTable<kRopeLow, D / 2> low;
+    } k;
+  } tables;
   __shared__ unsigned warp_top[kThreads / 32][HT];
   __shared__ unsigned cta_top[kMaxCluster][HT];
   if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {  // whole clusters
-    turn_queries<D>(p, table);
+    turn_queries<D>(p, tables.queries);
     return;
   }
   cg::cluster_group cluster = cg::this_cluster();
@@ -360,76 +363,81 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
   const bool turned = !is_v && grp < (p.rope.rot_dim >> 4);
   const int64_t vstride = (is_v ? p.v_stride : p.k_stride) / 8;
   const int mine = rank * CAP + rl;  // first row of this thread
-  const int step = ranks * CAP;      // rows of one pass of the cluster
   const uint4* src = reinterpret_cast<const uint4*>(is_v ? p.v : p.k) + (u.tok0 + mine) * vstride +
                      g * (D / 8);
-  uint4 a[kRowHeads], b[kRowHeads];
-  auto fetch = [&](int base) {
+  uint4 a[RT][HT], b[RT][HT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const uint4* row = src + base * vstride + i * (RL * vstride);
-      const bool in = base + mine + i * RL < u.rows;
-#pragma unroll
-      for (int h = 0; h < HT; ++h) {
-        a[i * HT + h] = b[i * HT + h] = make_uint4(0, 0, 0, 0);
-        if (in) {
-          a[i * HT + h] = __ldg(row + h * (D / 8) + at.x);
-          b[i * HT + h] = __ldg(row + h * (D / 8) + at.y);
-        }
-      }
-    }
-  };
-  auto turn = [&](int base) {
-    if (!turned) return;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      if (base + mine + i * RL >= u.rows) continue;
-      const int pos = __ldg(p.positions + u.tok0 + base + mine + i * RL);
-      RopeTurns cs;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        set_turn(cs, e, rope_turn(pos, rates_of(table)[8 * grp + e], p.rope.amplitude));
-#pragma unroll
-      for (int h = 0; h < HT; ++h) rope_group(a[i * HT + h], b[i * HT + h], cs, p.rope.interleaved != 0);
-    }
-  };
-
-  unsigned top[HT];
-#pragma unroll
-  for (int h = 0; h < HT; ++h) top[h] = 0;
-  float old[HT];
-  const int passes = (u.rows + step - 1) / step;  // 1 up to 8 CTAs' rows; more: read twice
-  const int64_t scale_row = static_cast<int64_t>(u.id) * p.num_kv_heads + g;
-  float* scales = is_v ? p.v_scales : p.k_scales;
-  for (int c = 0; c < passes; ++c) {
-    fetch(c * step);
-    if (c == 0) {
-      if (u.id < 0 || u.id >= p.num_blocks) {
-        if (tid == 0 && rank == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
-        return;
-      }
-#pragma unroll
-      for (int h = 0; h < HT; ++h) old[h] = u.r0 ? __ldcg(scales + scale_row + h) : 0.f;
-      // the rates of the frequencies, once per CTA (in the queries' table, unused here)
-      if (!is_v && tid < (p.rope.rot_dim >> 1))
-        rates_of(table)[tid] = rope_rate(__ldg(p.rope.inv_freq + tid));
-      __syncthreads();
-    }
-    turn(c * step);
+  for (int i = 0; i < RT; ++i) {
+    const uint4* row = src + i * (RL * vstride);
+    const bool in = mine + i * RL < u.rows;
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
-      uint4 ah[RT], bh[RT];
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        ah[i] = a[i * HT + h];
-        bh[i] = b[i * HT + h];
+      a[i][h] = b[i][h] = make_uint4(0, 0, 0, 0);
+      if (in) {
+        a[i][h] = __ldg(row + h * (D / 8) + at.x);
+        b[i][h] = __ldg(row + h * (D / 8) + at.y);
       }
-      top[h] = max(top[h], top_of(ah, bh));
     }
   }
+  if (u.id < 0 || u.id >= p.num_blocks) {
+    if (tid == 0 && rank == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+    return;
+  }
+  const int64_t scale_row = static_cast<int64_t>(u.id) * p.num_kv_heads + g;
+  float* scales = is_v ? p.v_scales : p.k_scales;
+  float old[HT];
+#pragma unroll
+  for (int h = 0; h < HT; ++h) old[h] = u.r0 ? __ldcg(scales + scale_row + h) : 0.f;
+
+  const int half = p.rope.rot_dim >> 1;
+  if (!is_v && half > 0 && rank * CAP < u.rows) {
+    // both factors of the CTA's positions, while its rows are on their way
+    const int32_t* pos = p.positions + u.tok0;
+    const int base = __ldg(pos + rank * CAP) & ~(kRopeLow - 1);
+    // one frequency per thread, rows `apart` apart
+    const int apart = kThreads / half, row0 = tid / half, f = tid - row0 * half;
+    if (row0 < apart) {
+      const unsigned long long rate = rope_rate(__ldg(p.rope.inv_freq + f));
+      for (int row = row0; row < kRopeLow; row += apart) tables.k.low.put(row, f, rope_low(row, rate));
+      for (int row = row0; row < HIGH; row += apart)
+        tables.k.high.put(row, f, rope_high(base + row * kRopeLow, rate, p.rope.amplitude));
+    }
+    __syncthreads();
+    if (turned) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        if (mine + i * RL >= u.rows) continue;
+        const int at_pos = __ldg(pos + mine + i * RL);
+        const unsigned high = static_cast<unsigned>(at_pos - base) / kRopeLow;
+        RopeTurns cs;
+        if (high < HIGH) {
+          cs = rope_product(tables.k.high.group(high, grp),
+                            tables.k.low.group(at_pos & (kRopeLow - 1), grp));
+        } else {
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e) {
+            const float2 t = rope_turn(at_pos, rope_rate(__ldg(p.rope.inv_freq + 8 * grp + e)),
+                                       p.rope.amplitude);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k == e) set_turn(cs, k, t);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < HT; ++h) rope_group(a[i][h], b[i][h], cs, p.rope.interleaved != 0);
+      }
+    }
+  }
+
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
-    const unsigned t = __reduce_max_sync(0xffffffffu, top[h]);
+    uint4 ah[RT], bh[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      ah[i] = a[i][h];
+      bh[i] = b[i][h];
+    }
+    const unsigned t = __reduce_max_sync(0xffffffffu, top_of(ah, bh));
     if ((tid & 31) == 0) warp_top[tid >> 5][h] = t;
   }
   __syncthreads();
@@ -443,7 +451,10 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
     }
     cluster.sync();
   }
-  float scale[HT];
+  uint8_t* codes = (is_v ? p.v_codes : p.k_codes) +
+                   ((static_cast<int64_t>(u.id) << p.bs_log2) * p.num_kv_heads + g) * D;
+  const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D;
+  uint8_t* first = codes + (u.r0 + mine) * row_bytes;
 #pragma unroll
   for (int h = 0; h < HT; ++h) {
     unsigned t = 0;
@@ -454,36 +465,21 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
       for (int w = 0; w < kThreads / 32; ++w) t = max(t, warp_top[w][h]);
     }
     const float need = exp2_int(scale_exponent(t));
-    scale[h] = old[h] >= need ? old[h] : need;  // old is 0 for a block that starts here
-    if (tid == 0 && rank == 0 && scale[h] != old[h]) scales[scale_row + h] = scale[h];
-  }
-  uint8_t* codes = (is_v ? p.v_codes : p.k_codes) +
-                   ((static_cast<int64_t>(u.id) << p.bs_log2) * p.num_kv_heads + g) * D;
-  const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D;
-  for (int c = passes - 1;; --c) {
-    uint8_t* first = codes + (u.r0 + c * step + mine) * row_bytes;
+    const float scale = old[h] >= need ? old[h] : need;  // old is 0 for a block that starts here
+    if (tid == 0 && rank == 0 && scale != old[h]) scales[scale_row + h] = scale;
+    const float inv = __frcp_rn(scale);
 #pragma unroll
-    for (int h = 0; h < HT; ++h) {
-      const float inv = __frcp_rn(scale[h]);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        if (c * step + mine + i * RL < u.rows) {
-          uint8_t* dst = first + i * (RL * row_bytes) + h * D;
-          *reinterpret_cast<uint2*>(dst + at.x * 8) = quantise8(a[i * HT + h], inv);
-          *reinterpret_cast<uint2*>(dst + at.y * 8) = quantise8(b[i * HT + h], inv);
-        }
+    for (int i = 0; i < RT; ++i) {
+      if (mine + i * RL < u.rows) {
+        uint8_t* dst = first + i * (RL * row_bytes) + h * D;
+        *reinterpret_cast<uint2*>(dst + at.x * 8) = quantise8(a[i][h], inv);
+        *reinterpret_cast<uint2*>(dst + at.y * 8) = quantise8(b[i][h], inv);
       }
     }
-    if (c == 0) break;
-    fetch((c - 1) * step);
-    turn((c - 1) * step);
-  }
-  if (u.r0 > 0) {
-#pragma unroll
-    for (int h = 0; h < HT; ++h)
-      if (scale[h] != old[h])
-        requantise_rows<D>(codes + h * D, row_bytes, u.r0, __fdiv_rn(old[h], scale[h]),
-                           rank * kThreads + tid, ranks * kThreads);
+    // rows that were in the block before, when its scale grew
+    if (u.r0 > 0 && scale != old[h])
+      requantise_rows<D>(codes + h * D, row_bytes, u.r0, __fdiv_rn(old[h], scale),
+                         rank * kThreads + tid, ranks * kThreads);
   }
 }
 
@@ -491,7 +487,8 @@ template <int D, int HT>
 cudaError_t launch_many(AppendParams p, int rows, cudaStream_t stream) {
   constexpr int CAP = kThreads / (D / 16) * (kRowHeads / HT);
   p.cluster = 1;
-  while (p.cluster < kMaxCluster && p.cluster * CAP < rows) p.cluster *= 2;
+  while (p.cluster * CAP < rows) p.cluster *= 2;
+  static_assert(kMaxCluster * (kThreads / (D / 16)) * kRowHeads >= 1024, "the largest block");
   p.q_ctas = (p.q_ctas + p.cluster - 1) / p.cluster * p.cluster;
   const int64_t grid = p.q_ctas + static_cast<int64_t>(p.num_seqs) * p.span * 2 *
                                       (p.num_kv_heads / HT) * p.cluster;
@@ -524,8 +521,9 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
     append_few_kernel<D><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
   }
-  if (p.num_kv_heads % 4 == 0) return launch_many<D, 4>(p, rows, stream);
-  if (p.num_kv_heads % 2 == 0) return launch_many<D, 2>(p, rows, stream);
+  constexpr int CAP = kThreads / (D / 16) * kRowHeads;  // rows of one head that a CTA holds
+  if (p.num_kv_heads % 4 == 0 && rows <= CAP / 4) return launch_many<D, 4>(p, rows, stream);
+  if (p.num_kv_heads % 2 == 0 && rows <= CAP / 2) return launch_many<D, 2>(p, rows, stream);
   return launch_many<D, 1>(p, rows, stream);
 }
 
