@@ -124,9 +124,19 @@ template <int D>
 __device__ __forceinline__ void requantise_rows(uint8_t* codes, int64_t row_bytes, int rows,
                                                 float factor, int first, int step) {
   constexpr int VPR = D / 16;  // 16-byte vectors of codes per row
-  for (int i = first; i < rows * VPR; i += step) {
-    uint4* at = reinterpret_cast<uint4*>(codes + (i / VPR) * row_bytes) + i % VPR;
-    *at = requantise16(*at, factor);
+  constexpr int U = 4;         // vectors in flight per thread
+  auto at = [&](int i) {
+    return reinterpret_cast<uint4*>(codes + (i / VPR) * row_bytes) + i % VPR;
+  };
+#pragma unroll 1
+  for (int i = first; i < rows * VPR; i += U * step) {
+    uint4 w[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (i + k * step < rows * VPR) w[k] = *at(i + k * step);
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (i + k * step < rows * VPR) *at(i + k * step) = requantise16(w[k], factor);
   }
 }
 
@@ -231,7 +241,117 @@ __device__ __forceinline__ unsigned top_of(const uint4 (&a)[N], const uint4 (&b)
   return max(top & 0xffffu, top >> 16);
 }
 
-// Few new rows per block (a decode step; blocks of 16 and 32): a warp per (sequence, block,
+// At most one new row per sequence (a decode step). CTA i takes the queries of token i and the
+// K and V rows of sequence i, a head per D / 16 threads: one table holds the turns of both
+// tokens (the same one, as a rule), and the few dependent reads (lengths, block id, old scale)
+// run beside the rows'.
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_one_kernel(const AppendParams p) {
+  constexpr int NG = D / 16;             // threads per head
+  constexpr int HL = kThreads / NG;      // heads side by side
+  constexpr int kMaxGrown = 128;         // K or V heads whose scale grew, of one pass over HL
+  __shared__ RopeTable<2, D / 2> table;  // row 0: the queries' token, row 1: the keys'
+  __shared__ int grown[HL];
+  __shared__ float factor[HL];
+  __shared__ int num_grown;
+  static_assert(HL <= kMaxGrown, "one entry per head of a pass");
+  const int tid = threadIdx.x;
+  const int i = blockIdx.x;
+  const int grp = tid % NG, hl = tid / NG;
+  const int2 at = rope_vectors(grp, p.rope);
+  const bool in_rot = grp < (p.rope.rot_dim >> 4);
+  Span u{};
+  const bool stored = i < p.num_seqs && find_span(p, i, 0, tid == 0, u);
+  const int q_heads = i < p.num_tokens ? p.num_q_heads : 0;
+  const int kv_heads = stored ? 2 * p.num_kv_heads : 0;  // K heads, then V heads
+  const int heads = q_heads + kv_heads;
+
+  // the first pass's vectors, then the turns
+  auto source = [&](int h) -> const uint4* {
+    if (h < q_heads) return reinterpret_cast<const uint4*>(p.q + i * p.q_stride + h * D);
+    h -= q_heads;
+    return h < p.num_kv_heads
+               ? reinterpret_cast<const uint4*>(p.k + u.tok0 * p.k_stride + h * D)
+               : reinterpret_cast<const uint4*>(p.v + u.tok0 * p.v_stride + (h - p.num_kv_heads) * D);
+  };
+  const bool good = stored && u.id >= 0 && u.id < p.num_blocks;
+  auto scale_of = [&](int kv) {  // kv: K head, or num_kv_heads + V head
+    return (kv < p.num_kv_heads ? p.k_scales + kv : p.v_scales + kv - p.num_kv_heads) +
+           static_cast<int64_t>(u.id) * p.num_kv_heads;
+  };
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  float old = 0.f;  // of a block that starts here
+  auto fetch = [&](int h) {
+    if (h >= heads) return;
+    a = __ldg(source(h) + at.x);
+    b = __ldg(source(h) + at.y);
+    old = h >= q_heads && good && u.r0 ? __ldcg(scale_of(h - q_heads)) : 0.f;
+  };
+  fetch(hl);
+  if (stored && !good && tid == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+  const int half = p.rope.rot_dim >> 1;
+  if (half > 0) {
+    // one (row, frequency) per thread and pass
+    for (int k = tid; k < 2 * half; k += kThreads) {
+      const int row = k / half, f = k - row * half;
+      if (row == 0 ? q_heads > 0 : good) {
+        const int pos = __ldg(p.positions + (row == 0 ? i : u.tok0));
+        table.put(row, f, rope_turn(pos, rope_rate(__ldg(p.rope.inv_freq + f)), p.rope.amplitude));
+      }
+    }
+  }
+  if (tid == 0) num_grown = 0;
+  __syncthreads();
+  const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D;
+  auto codes_of = [&](int kv) {
+    const bool is_v = kv >= p.num_kv_heads;
+    return (is_v ? p.v_codes : p.k_codes) +
+           ((static_cast<int64_t>(u.id) << p.bs_log2) * p.num_kv_heads + (is_v ? kv - p.num_kv_heads : kv)) * D;
+  };
+  for (int h0 = 0; h0 < heads; h0 += HL) {
+    const int h = h0 + hl, kv = h - q_heads;
+    const bool is_q = h < q_heads;
+    const bool row = h < heads && !is_q && good;
+    if (in_rot && (is_q || (row && kv < p.num_kv_heads)))
+      rope_group(a, b, table.group(is_q ? 0 : 1, grp), p.rope.interleaved != 0);
+    if (is_q) {
+      uint4* dst = reinterpret_cast<uint4*>(p.q_out + i * p.q_out_stride + h * D);
+      dst[at.x] = a;
+      dst[at.y] = b;
+    }
+    // the head's threads agree on its scale
+    const uint4 va[1] = {a}, vb[1] = {b};
+    unsigned amax = row ? top_of(va, vb) : 0;
+#pragma unroll
+    for (int o = NG / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    __syncwarp();  // every thread of a head has read its old scale
+    if (row) {
+      const float need = exp2_int(scale_exponent(amax));
+      const float scale = old >= need ? old : need;
+      const float inv = __frcp_rn(scale);
+      uint8_t* dst = codes_of(kv) + u.r0 * row_bytes;
+      *reinterpret_cast<uint2*>(dst + at.x * 8) = quantise8(a, inv);
+      *reinterpret_cast<uint2*>(dst + at.y * 8) = quantise8(b, inv);
+      if (scale != old && grp == 0) {
+        *scale_of(kv) = scale;
+        if (u.r0 > 0) {
+          const int n = atomicAdd(&num_grown, 1);
+          grown[n] = kv;
+          factor[n] = __fdiv_rn(old, scale);
+        }
+      }
+    }
+    fetch(h + HL);
+    // rows that were in the block before, when its scale grew: by the whole CTA
+    __syncthreads();
+    for (int n = 0; n < num_grown; ++n)
+      requantise_rows<D>(codes_of(grown[n]), row_bytes, u.r0, factor[n], tid, kThreads);
+    __syncthreads();
+    if (tid == 0) num_grown = 0;
+  }
+}
+
+// Few new rows per block (short chunks; blocks of 16 and 32): a warp per (sequence, block,
 // K or V, head), eight to a CTA.
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams p) {
@@ -514,6 +634,11 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
   if (!q_here) p.num_q_heads = 0;
   p.q_ctas = p.num_q_heads > 0 ? (p.num_tokens + kQTokens - 1) / kQTokens : 0;
   p.cluster = 1;
+  if (p.max_new == 1) {
+    const int grid = p.num_q_heads > 0 && p.num_tokens > p.num_seqs ? p.num_tokens : p.num_seqs;
+    append_one_kernel<D><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
   if (rows <= kFewRows) {
     const int64_t units = static_cast<int64_t>(p.num_seqs) * p.span * 2 * p.num_kv_heads;
     const int64_t grid = p.q_ctas + (units + kThreads / 32 - 1) / (kThreads / 32);

@@ -68,6 +68,9 @@ def same_codes(got, want):
 @pytest.mark.parametrize("hkv,d,bs,new,old", [
     (8, 128, 256, [1] * 6, [0, 1, 255, 256, 300, 37]),       # decode steps
     (2, 64, 16, [1, 1, 1], [0, 15, 16]),
+    (40, 128, 64, [1, 0, 1], [63, 5, 64]),                    # more heads than a pass, one idle
+    (3, 128, 1024, [1, 1], [1023, 1024]),
+    (8, 128, 64, [3, 1, 2], [62, 0, 31]),                     # a few rows each
     (2, 128, 16, [40, 0, 16, 7], [0, 5, 8, 9]),               # blocks of 16, one sequence idle
     (1, 128, 32, [33, 64, 95], [31, 0, 1]),
     (3, 128, 64, [61, 130, 1], [3, 63, 64]),
@@ -94,19 +97,25 @@ def test_append_matches_the_oracle_bit_for_bit(hkv, d, bs, new, old):
     assert same_codes(dv.cpu().numpy(), want_v[0])
 
 
-@pytest.mark.parametrize("inter,rot", [(False, 128), (True, 64), (False, 16)])
-@pytest.mark.parametrize("new,bs", [([1, 1, 1], 256), ([70, 3], 64)])
-def test_rope_append_equals_rope_then_append(new, bs, inter, rot):
+@pytest.mark.parametrize("inter,rot", [(False, 128), (True, 64), (False, 16), (True, 48), (False, 0)])
+@pytest.mark.parametrize("new,bs,steady", [([1, 1, 1], 256, True), ([1, 0, 1, 1], 64, True), ([70, 3], 64, False),
+                                           ([70, 3], 64, True), ([300, 129, 1000], 256, True), ([5, 20], 32, True),
+                                           ([1024 + 700], 1024, True), ([400], 512, False)])
+def test_rope_append_equals_rope_then_append(new, bs, steady, inter, rot):
+    """steady: positions follow one another, as a rule; else they are anywhere."""
     rng = np.random.default_rng(rot + bs)
-    hq, hkv, d = 4, 2, 128
+    hq, hkv, d = 4, (1 if bs == 512 else 2), 128
     ctx = np.array(new) + 13
     tables, nb = tables_of(rng, ctx, bs)
     cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     T = int(cu[-1])
     qkv = bf16_dev(f32_to_bf16_bits(rng.standard_normal((T, hq + 2 * hkv, d)).astype(np.float32)))
     q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
-    pos = i32_dev(rng.integers(0, 2 ** 20, T))
-    f = torch.tensor(pa.pa_rope_inv_freq(rot)[0], dtype=torch.float32, device="cuda")
+    pos = rng.integers(-2 ** 20, 2 ** 30, T)
+    if steady:
+        pos = np.concatenate([rng.integers(-300, 10 ** 6) + np.arange(n) for n in new])
+    pos = i32_dev(pos)
+    f = torch.tensor(pa.pa_rope_inv_freq(rot)[0] if rot else [], dtype=torch.float32, device="cuda")
     kc, ks = pools_of(rng, nb, bs, hkv, d)
     vc, vs = pools_of(rng, nb, bs, hkv, d)
     a = [u8_dev(kc), u8_dev(vc), f32_dev(ks), f32_dev(vs)]
