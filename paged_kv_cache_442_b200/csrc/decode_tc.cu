@@ -1077,9 +1077,12 @@ __global__ void __launch_bounds__(kThreadsOf<G, F8>, 1) decode_tc_kernel(
           // A parity wait is only sound once the phase before it is known to be complete.
           // The P buffer's wait above covers V tile j - NP, which is older than this
           // slot's last one (j - NV): a V load slower than the score path would make the
-          // wait below pass at once, clear the older tile and leave this one's rows.
-          if (j >= NV)
-            failed |= !wait_or_abort(&v_full[vs], ((j / NV) - 1) & 1, p.err, abort_flag, wl);
+          // wait below pass at once, clear the older tile and leave this one's rows. The
+          // value product of tile j - NV read that tile, so it had landed.
+          if (j >= NV) {
+            const unsigned t = j - NV;
+            failed |= !wait_or_abort(&pv_done[t % NP], (t / NP) & 1, p.err, abort_flag, wl);
+          }
           failed |= !wait_or_abort(&v_full[vs], (j / NV) & 1, p.err, abort_flag, wl);
 #pragma unroll
           for (int u = 0; u < SUB; ++u) {

@@ -1,11 +1,12 @@
 """The waits of the persistent decode by parity, on a model of the barriers.
 
-An mbarrier wait names a phase only by its parity: asked for phase k while phase k - 1 is
-still open, it answers "complete" because phase k - 2 has the same parity. The decode's
-softmax clears the rows past a partition's end in the V slot of tile j, after waiting for
-that tile. Its P buffers (NP of them) prove that V tile j - NP has landed; the slot's
-previous tile is j - NV. With NP > NV the previous tile may still be on its way, so the
-wait needs the previous phase first.
+An mbarrier wait names a phase only by its parity. Asked for phase k while phase k - 1 is
+still open it answers "complete" at once (phase k - 2 has the same parity), and asked for
+phase k - 1 once phase k is complete as well it waits for phase k + 1. The decode's softmax
+clears the rows past a partition's end in the V slot of tile j, after waiting for that tile.
+Its P buffers (NP of them) prove that V tile j - NP has landed; the slot's previous tile is
+j - NV. With NP > NV that tile may still be on its way, so the softmax first waits for the
+value product that read it, on a barrier whose phases it has followed.
 """
 import os
 import re
@@ -17,40 +18,58 @@ from paged_kv_cache_442_b200 import build as pa_build
 NV, NP = 3, 4
 
 
-class Barrier:
-    """Completed phases of one ring slot; wait(k) answers as try_wait.parity does."""
-
-    def __init__(self, completed):
-        self.completed = completed
-
-    def passes(self, phase):
-        return (self.completed & 1) != (phase & 1)
+def passes(completed, phase):
+    """try_wait.parity on a barrier with `completed` phases behind it."""
+    return (completed & 1) != (phase & 1)
 
 
-def landed_when_the_wait_passes(j, oldest_missing, waits):
-    """Tile j's wait(s) while V tiles from `oldest_missing` on are still in flight: does
-    every wait that passes mean that tile j has landed?"""
-    slot_tiles = [t for t in range(j + 1) if t % NV == j % NV]
-    done = sum(t < oldest_missing for t in slot_tiles)
-    bar = Barrier(done)
-    passed = all(bar.passes(ph) for ph in waits)
-    return (not passed) or done == len(slot_tiles)
+def phases(ring, j, done):
+    """Completed phases of tile j's slot when the tiles 0 .. done - 1 are done, in order."""
+    return sum(t < done for t in range(j % ring, done + ring, ring) if t < done)
 
 
-@pytest.mark.parametrize("j", range(NV, 24))
-def test_waiting_for_the_previous_phase_first_is_sound(j):
-    # pv_done of tile j - NP has been waited for: V tiles up to j - NP have landed
-    for missing in range(max(0, j - NP + 1), j + 2):
-        assert landed_when_the_wait_passes(j, missing, [j // NV - 1, j // NV])
+def guarded(j, landed, produced):
+    """(does the guarded wait pass, is it right to) for V tiles 0 .. landed - 1 in shared
+    memory and value products 0 .. produced - 1 done (each needs its tile)."""
+    t = j - NV
+    if t >= 0 and not passes(phases(NP, t, produced), t // NP):
+        return False, True
+    ok = passes(phases(NV, j, landed), j // NV)
+    return ok, (not ok) or landed > j
 
 
-def test_the_single_wait_is_not():
-    assert not landed_when_the_wait_passes(7, 7 - NV, [7 // NV])
+@pytest.mark.parametrize("j", range(0, 24))
+def test_the_guarded_wait_is_sound_and_ends(j):
+    # tile j's P buffer was last read by tile j - NP: that product is done; tile j's own
+    # product waits for the softmax, so at most j products are
+    for produced in range(max(0, j - NP + 1), j + 1):
+        for landed in range(produced, j + 2):
+            if landed > produced + NV:      # a V slot is refilled once its product is done
+                continue
+            ok, right = guarded(j, landed, produced)
+            assert right
+            if produced > j - NV and landed > j:
+                assert ok                   # nothing left to wait for
 
 
-def test_the_kernel_waits_for_both_phases():
+def test_a_bare_wait_is_not_sound():
+    # V tile 4 of slot 1 still on its way: the wait for tile 7 passes all the same
+    assert passes(phases(NV, 7, 4), 7 // NV)
+
+
+def test_waiting_for_the_slot_s_previous_phase_may_never_end():
+    # tiles 4 and 7 have both landed: phase 4 // NV asked for afterwards waits for tile 10
+    assert not passes(phases(NV, 7, 8), 7 // NV - 1)
+
+
+def test_the_kernel_guards_its_wait():
     src = open(os.path.join(pa_build.CSRC, "decode_tc.cu")).read()
     ring = dict(re.findall(r"constexpr int (N[PV]) = (\d+);", src))
     assert int(ring["NP"]) == NP and int(ring["NV"]) == NV
-    waits = re.findall(r"failed \|= !wait_or_abort\(&v_full\[vs\], \(([^&]+)\) & 1", src)
-    assert waits == ["(j / NV) - 1", "j / NV"]
+    at = src.index("failed |= !wait_or_abort(&v_full[vs]")
+    assert re.search(r"t = j - NV;\s+failed \|= !wait_or_abort\(&pv_done\[t % NP\], \(t / NP\) & 1", src[at - 400:at])
+
+
+def test_the_block_scale_decode_needs_no_guard():
+    src = open(os.path.join(pa_build.CSRC, "decode_blockscale.cu")).read()
+    assert "static_assert(NP <= NV" in src
