@@ -1094,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) {
             fence_acq_rel_gpu();
             bool okc = true;
-            const unsigned before = tagged_arrive_many(ctr, p.tag, p.err, &okc);
+            const unsigned before = tagged_arrive(ctr, p.tag, p.err, &okc);
             const bool is_last = okc && before == static_cast<unsigned>(total - 1);
             if (is_last) *reinterpret_cast<volatile unsigned long long*>(ctr) = 0ull;
             *last_flag = is_last;

@@ -43,28 +43,6 @@ __device__ __forceinline__ unsigned tagged_fetch_add(unsigned long long* ctr,
   return static_cast<unsigned>(old & kCountMask);
 }
 
-// Same contract as tagged_fetch_add for a counter that only a few threads ever touch
-// (the arrivals of one sequence's partitions): add first, and only if the tag was
-// stale try to restart the count under this call's tag. With so few contenders this
-// is one atomic in the common case. Bounded number of attempts.
-__device__ __forceinline__ unsigned tagged_arrive(unsigned long long* ctr, unsigned long long tag,
-                                                  unsigned* err, bool* ok) {
-  for (int it = 0; it < 4096; ++it) {
-    const unsigned long long old = atomicAdd(ctr, 1ull);
-    if ((old >> kCountBits) == tag) {
-      *ok = true;
-      return static_cast<unsigned>(old & kCountMask);
-    }
-    if (atomicCAS(ctr, old + 1, (tag << kCountBits) | 1ull) == old + 1) {
-      *ok = true;
-      return 0u;
-    }
-  }
-  flag_error(err, PA_DEV_ERR_TIMEOUT);
-  *ok = false;
-  return 0;
-}
-
 // Give a counter this call's tag with count 0 unless it has the tag already. Everyone who
 // finds a stale value swaps in the same one, so a failed swap means that another thread
 // (or one of its adds, at most one per thread) came first: no two can keep each other busy.
@@ -83,12 +61,13 @@ __device__ __forceinline__ bool tagged_install(unsigned long long* ctr, unsigned
   return true;
 }
 
-// tagged_arrive for many simultaneous contenders on a counter whose tag was most likely
-// installed ahead (tagged_install): one atomic when it was. With a stale tag the first add
-// lands on a value that the installation replaces, and is made again.
-__device__ __forceinline__ unsigned tagged_arrive_many(unsigned long long* ctr,
-                                                       unsigned long long tag, unsigned* err,
-                                                       bool* ok) {
+// Same contract as tagged_fetch_add for the arrivals of an item's parts: add first (one atomic
+// once the tag is there); with a stale tag that add lands on a value that the installation
+// replaces, and is made again. (Adding and swapping in (tag, 1) in turn until one of the two
+// holds let sixteen simultaneous arrivals disturb one another for thousands of rounds.)
+__device__ __forceinline__ unsigned tagged_arrive(unsigned long long* ctr,
+                                                  unsigned long long tag, unsigned* err,
+                                                  bool* ok) {
   unsigned long long old = atomicAdd(ctr, 1ull);
   *ok = true;
   if ((old >> kCountBits) != tag) {
