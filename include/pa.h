@@ -539,8 +539,9 @@ pa_status pa_rope_store_kvcache_fp8_blockscale(
 
 /*
  * pa_decode_fp8_blockscale — pa_decode over e4m3 pools with block scales: one query token
- * per sequence attends over the values the pools hold (code * scale; scales any finite
- * fp32 >= 0). The tensor cores read the codes as they are stored; q reaches them as three
+ * per sequence attends over the values the pools hold (code * scale; a scale is 0 or any
+ * fp32 from 2^-126 up to where 448 * scale still is finite). The tensor cores read the codes
+ * as they are stored; q reaches them as three
  * e4m3 terms (about 2^-13 relative per element), the probabilities, times their block's V
  * scale over the largest one of the part, as two (about 2^-8 relative; below 2^-10 of the
  * part's largest product of probability and V scale the error is absolute, about 2^-18 of

@@ -447,6 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (tid == 12 * 32) {
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmKt);
+  }
+  if (tid == 13 * 32) {
+    prefetch_tensormap(&tmV);
+    prefetch_tensormap(&tmVt);
+  }
   // q slots and P buffers start at zero: rows that no head uses stay zero
 #pragma unroll 1
   for (int i = tid; i < (QN * C::kQBytes + NP * C::kPBytes) / 16; i += kThreads)
@@ -489,8 +497,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idO = idesc_e4m3_f32(HD, NPR, 1, 0);  // V^T MN-major, P terms K-major
     const uint64_t ring_desc = smem_desc_sw128(smem_u32(ring), is_v ? kHalf : 16, 1024);
     const uint64_t b_desc = smem_desc_sw128(smem_u32(smem + (is_v ? C::kOffP : C::kOffQ)), 16, 1024);
-    if (lane == 0) prefetch_tensormap(map);
-    __syncwarp();
     const int rows_log2 = bs < TT ? p.bs_log2 : 8;   // rows per box of a full tile
     const int trows_log2 = bs < 32 ? p.bs_log2 : 5;  // of a context's last tile (none past it)
     unsigned jl = 0, jm = 0;              // tiles whose load / product was issued
@@ -771,9 +777,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 8) {
     // ======================================================== softmax
     // Thread r of group sg owns position 128 sg + r of each tile. Control flow is uniform
-    // over the 256 threads: a failed wait only marks `failed`, and the barrier that every
-    // tile has (the exchange of maxima) votes on it before anything of the tile's record
-    // decides a branch around a barrier.
+    // over the 256 threads: a failed wait only marks `failed`, and the vote that every tile
+    // has settles it before anything of the tile's record decides a branch around a barrier.
     const int sg = warp >> 2;
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
@@ -990,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // empty contexts: a zero row for every head
 #pragma unroll 1
     for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x)
-      if (__ldg(p.context_lens + s) <= 0)
+      if (p.max_context_len == 0 || __ldg(p.context_lens + s) <= 0)
 #pragma unroll 1
         for (int i = dl; i < Hq * HD / 2; i += 128)
           reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(s) * Hq * HD)[i] = 0u;

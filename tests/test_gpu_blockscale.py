@@ -211,7 +211,7 @@ def close(gpu, ref, what=""):
 @pytest.mark.parametrize("ctx,hq,hkv,bs", [
     ([1], 1, 1, 16), ([5, 0, 256, 257, -3, 31], 4, 2, 16), ([512], 8, 8, 32), ([100, 700, 33], 16, 8, 256),
     ([1000, 1, 2047, 64], 32, 8, 64), ([300, 300], 16, 1, 128), ([700, 129], 32, 2, 16), ([1025, 600], 3, 3, 512),
-    ([2500, 1024], 6, 6, 1024), ([9000], 8, 1, 128), ([0, 0], 4, 2, 64), ([40] * 70, 4, 4, 16),
+    ([2500, 1024], 6, 6, 1024), ([9000], 8, 1, 128), ([1, 255, 256, 1023, 5], 2, 2, 1024), ([30000], 1, 1, 32), ([0, 0], 4, 2, 64), ([40] * 70, 4, 4, 16),
     ([20000], 2, 1, 16), ([6001, 17], 16, 4, 256),
 ])
 def test_decode_matches_the_oracle(ctx, hq, hkv, bs):
@@ -321,6 +321,28 @@ def test_decode_bad_block_id_and_too_long_a_context_are_reported():
     assert e.value.status == 3
     d.ctx = np.array([400, 90], np.int32)      # clipped to the host's bound
     close(out, d.oracle())
+
+
+def test_decode_clipped_to_nothing_gives_zeros():
+    c = Case([70, 0, 300], 4, 2, 64, seed=5)
+    out = torch.full((3, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(pa.PAError) as e:
+        c.gpu(max_ctx=0, out=out)
+    assert e.value.status == 3
+    assert not out.any()
+
+
+def test_decode_not_a_number_stays_in_its_head():
+    """A NaN in one query head reaches that head's output only; NaN and infinite rows past a
+    context reach none (every Case has them)."""
+    c = Case([700, 40], 4, 2, 64, seed=6)
+    ok = c.gpu()
+    c.dev[0][0, 1, 5] = float("nan")
+    out = c.gpu()
+    assert torch.isnan(out[0, 1].float()).all()
+    same = torch.ones(2, 4, dtype=torch.bool)
+    same[0, 1] = False
+    assert torch.equal(out[same.cuda()].view(torch.int16), ok[same.cuda()].view(torch.int16))
 
 
 def test_decode_wait_that_runs_out_is_reported():
