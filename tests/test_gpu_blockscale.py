@@ -76,6 +76,10 @@ def same_codes(got, want):
     (3, 128, 64, [61, 130, 1], [3, 63, 64]),
     (2, 128, 256, [600, 256], [10, 0]),                       # whole blocks in registers
     (1, 64, 512, [700], [100]),
+    (8, 128, 256, [700, 513, 0, 900], [10, 255, 5, 256]),     # many units per SM
+    (4, 128, 64, [3000, 200], [63, 5]),
+    (2, 64, 128, [2500, 77], [100, 127]),
+    (3, 128, 256, [3000], [1]),
     (2, 128, 1024, [1500, 900], [700, 0]),                    # blocks read twice
 ])
 def test_append_matches_the_oracle_bit_for_bit(hkv, d, bs, new, old):
