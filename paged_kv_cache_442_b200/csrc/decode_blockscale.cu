@@ -70,6 +70,11 @@ constexpr int kSoftThreads = 256;
 constexpr int kFan = 16;       // parts merged at a time
 constexpr int kTileCost = 8;   // of a full tile, in units of 32 positions
 constexpr int kTailCost = 4;   // least of a context's last tile
+// Longest context, in tiles, that is left whole when every item can have a group of its own: the
+// merge of a split item costs about a tile's time. Whole against split, us: 4 sequences of 512
+// positions, 2 q heads a kv head 8.0 / 9.0, 16 of 512 8.7 / 10.4; at 768 positions the two are
+// equal (10.0 / 10.1), at 1024 four sequences want the split (11.1 / 10.4, 8 q heads 13.0 / 11.3).
+constexpr int kWholeTiles = 2;
 constexpr int kItemCost = 5;   // an item's own (its q terms, first reference and epilogue)
 constexpr float kTarget = 3.f;  // a new reference puts the largest P' at 2^kTarget ...
 constexpr float kBound = 6.f;   // ... and it moves when one would pass 2^kBound (128 (P' - hi)
@@ -354,8 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return ctx > 0 ? ctx : 0;
   };
+  bool whole = false;  // no item is split
   auto cost_of = [&](int ctx) -> unsigned {
     if (ctx == 0) return 0;
+    if (whole) return kTileCost;
     const int tiles = (ctx + TT - 1) / TT;
     const int tail = (ctx - (tiles - 1) * TT + 31) / 32;
     return static_cast<unsigned>((tiles - 1) * kTileCost + (tail > kTailCost ? tail : kTailCost) + kItemCost);
@@ -414,15 +421,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int second = context(32 + lane);  // read beside the window's
     window();
     cost = wtotal;
+    unsigned items = __popc(__ballot_sync(0xffffffffu, wctx > 0));
+    int longest = wctx;
     if (p.num_seqs > 32) {
-      unsigned sum = cost_of(second);
+      unsigned sum = cost_of(second), count = second > 0;
+      longest = max(longest, second);
 #pragma unroll 1
-      for (int s = 64 + lane; s < p.num_seqs; s += 32) sum += cost_of(context(s));
+      for (int s = 64 + lane; s < p.num_seqs; s += 32) {
+        const int ctx = context(s);
+        sum += cost_of(ctx);
+        count += ctx > 0;
+        longest = max(longest, ctx);
+      }
       cost += __reduce_add_sync(0xffffffffu, sum) * hgroups;
+      items += __reduce_add_sync(0xffffffffu, count);
     }
-    // runs at least a tile long: no run is skipped between two tiles of an item
-    const unsigned most = cost / kTileCost;
-    const unsigned groups = most < static_cast<unsigned>(p.groups) ? (most ? most : 1) : p.groups;
+    items *= hgroups;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    unsigned groups;
+    if (items > 0 && items <= static_cast<unsigned>(p.groups) && longest <= kWholeTiles * TT) {
+      // few short contexts: a group each (every item counts as one tile in the split)
+      whole = true;
+      groups = items;
+      cost = items * kTileCost;
+      window();
+    } else {
+      // runs at least a tile long: no run is skipped between two tiles of an item
+      const unsigned most = cost / kTileCost;
+      groups = most < static_cast<unsigned>(p.groups) ? (most ? most : 1) : p.groups;
+    }
     if (cost > 0 && static_cast<unsigned>(group) < groups) {
       run_q = cost / groups;
       run_r = cost - run_q * groups;
@@ -640,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int g = it.hg * p.members + member;
       const int tiles = (it.ctx + TT - 1) / TT;
       const int upto = static_cast<int>((run_end - it.cum + kTileCost - 1) / kTileCost);
-      const int tb = tiles < upto ? tiles : upto;
+      const int tb = tiles < upto || whole ? tiles : upto;
       more = it.cum + it.cost < run_end;
       float ref = 0.f;
       float ksc = 0.f, vsc = 0.f;
@@ -695,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int group0 = group_of(it.cum);
             rec.group0 = group0;
             rec.part = group - group0;
-            rec.nparts = group_of(it.cum + (tiles - 1) * kTileCost) - group0 + 1;
+            rec.nparts = whole ? 1 : group_of(it.cum + (tiles - 1) * kTileCost) - group0 + 1;
           }
           rec.ref = now;
           rec.alpha = (t == ta || now == ref || ref == 0.f) ? 1.f : __fdividef(ref, now);

@@ -223,6 +223,16 @@ def test_decode_matches_the_oracle(ctx, hq, hkv, bs):
     close(c.gpu(), c.oracle(), f"{ctx[:4]} {hq}/{hkv} {bs}")
 
 
+@pytest.mark.parametrize("ctx,hq,hkv,bs", [
+    ([512, 0, 511, 257, 1], 16, 8, 64), ([513, 0, 511, 257, 1], 16, 8, 64),   # each item whole; one split
+    ([512] * 36, 8, 4, 128), ([512] * 38, 8, 4, 128),                         # as many items as groups; more
+    ([3, 0, 0, 500] * 18, 4, 1, 16), ([0] * 33 + [512, 0, 400], 32, 2, 256),  # beyond a window of 32
+])
+def test_decode_short_contexts_whole_and_split(ctx, hq, hkv, bs):
+    c = Case(ctx, hq, hkv, bs, seed=sum(ctx) + bs)
+    close(c.gpu(), c.oracle(), f"{len(ctx)} x {max(ctx)} {hq}/{hkv} {bs}")
+
+
 @pytest.mark.parametrize("g", [1, 2, 4, 8, 16])
 @pytest.mark.parametrize("q_factor,spread", [(8.0, 0.3), (0.0, 2.0), (30.0, 1.0)])
 def test_decode_peaked_flat_and_uneven_scales(g, q_factor, spread):
