@@ -249,12 +249,10 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) append_one_kernel(const AppendParams p) {
   constexpr int NG = D / 16;             // threads per head
   constexpr int HL = kThreads / NG;      // heads side by side
-  constexpr int kMaxGrown = 128;         // K or V heads whose scale grew, of one pass over HL
   __shared__ RopeTable<2, D / 2> table;  // row 0: the queries' token, row 1: the keys'
-  __shared__ int grown[HL];
+  __shared__ int grown[HL];              // K or V heads of a pass whose scale grew
   __shared__ float factor[HL];
-  __shared__ int num_grown;
-  static_assert(HL <= kMaxGrown, "one entry per head of a pass");
+  __shared__ int num_grown[2];           // of even and odd passes
   const int tid = threadIdx.x;
   const int i = blockIdx.x;
   const int grp = tid % NG, hl = tid / NG;
@@ -300,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const AppendParams
       }
     }
   }
-  if (tid == 0) num_grown = 0;
+  if (tid < 2) num_grown[tid] = 0;
   __syncthreads();
   const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D;
   auto codes_of = [&](int kv) {
@@ -308,7 +306,8 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const AppendParams
     return (is_v ? p.v_codes : p.k_codes) +
            ((static_cast<int64_t>(u.id) << p.bs_log2) * p.num_kv_heads + (is_v ? kv - p.num_kv_heads : kv)) * D;
   };
-  for (int h0 = 0; h0 < heads; h0 += HL) {
+  int odd = 0;
+  for (int h0 = 0; h0 < heads; h0 += HL, odd ^= 1) {
     const int h = h0 + hl, kv = h - q_heads;
     const bool is_q = h < q_heads;
     const bool row = h < heads && !is_q && good;
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const AppendParams
       if (scale != old && grp == 0) {
         *scale_of(kv) = scale;
         if (u.r0 > 0) {
-          const int n = atomicAdd(&num_grown, 1);
+          const int n = atomicAdd(&num_grown[odd], 1);
           grown[n] = kv;
           factor[n] = __fdiv_rn(old, scale);
         }
@@ -344,10 +343,11 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const AppendParams
     fetch(h + HL);
     // rows that were in the block before, when its scale grew: by the whole CTA
     __syncthreads();
-    for (int n = 0; n < num_grown; ++n)
+    // the next pass counts in the other word, last read before the barrier that ended its pass
+    if (tid == 0) num_grown[odd ^ 1] = 0;
+    for (int n = 0; n < num_grown[odd]; ++n)
       requantise_rows<D>(codes_of(grown[n]), row_bytes, u.r0, factor[n], tid, kThreads);
     __syncthreads();
-    if (tid == 0) num_grown = 0;
   }
 }
 

@@ -69,6 +69,7 @@ def same_codes(got, want):
     (8, 128, 256, [1] * 6, [0, 1, 255, 256, 300, 37]),       # decode steps
     (2, 64, 16, [1, 1, 1], [0, 15, 16]),
     (40, 128, 64, [1, 0, 1], [63, 5, 64]),                    # more heads than a pass, one idle
+    (96, 128, 16, [1] * 48, list(range(1, 49))),              # scales grow in pass after pass
     (3, 128, 1024, [1, 1], [1023, 1024]),
     (8, 128, 64, [3, 1, 2], [62, 0, 31]),                     # a few rows each
     (2, 128, 16, [40, 0, 16, 7], [0, 5, 8, 9]),               # blocks of 16, one sequence idle
