@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
     if (tid == 0 && rank == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
     return;
   }
+  if (ranks > 1) cluster.barrier_arrive();  // this CTA runs: its shared memory may be written
   const int64_t scale_row = static_cast<int64_t>(u.id) * p.num_kv_heads + g;
   float* scales = is_v ? p.v_scales : p.k_scales;
   float old[HT];
@@ -513,14 +514,14 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
   if (!is_v && half > 0 && rank * CAP < u.rows) {
     // both factors of the CTA's positions, while its rows are on their way
     const int32_t* pos = p.positions + u.tok0;
-    const int base = __ldg(pos + rank * CAP) & ~(kRopeLow - 1);
+    const unsigned base = static_cast<unsigned>(__ldg(pos + rank * CAP)) & ~(kRopeLow - 1u);
     // one frequency per thread, rows `apart` apart
     const int apart = kThreads / half, row0 = tid / half, f = tid - row0 * half;
     if (row0 < apart) {
       const unsigned long long rate = rope_rate(__ldg(p.rope.inv_freq + f));
       for (int row = row0; row < kRopeLow; row += apart) tables.k.low.put(row, f, rope_low(row, rate));
       for (int row = row0; row < HIGH; row += apart)
-        tables.k.high.put(row, f, rope_high(base + row * kRopeLow, rate, p.rope.amplitude));
+        tables.k.high.put(row, f, rope_high(static_cast<int>(base + row * kRopeLow), rate, p.rope.amplitude));
     }
     __syncthreads();
     if (turned) {
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
       for (int i = 0; i < RT; ++i) {
         if (mine + i * RL >= u.rows) continue;
         const int at_pos = __ldg(pos + mine + i * RL);
-        const unsigned high = static_cast<unsigned>(at_pos - base) / kRopeLow;
+        const unsigned high = (static_cast<unsigned>(at_pos) - base) / kRopeLow;
         RopeTurns cs;
         if (high < HIGH) {
           cs = rope_product(tables.k.high.group(high, grp),
@@ -562,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
   }
   __syncthreads();
   if (ranks > 1) {
+    cluster.barrier_wait();  // every CTA of the cluster runs
     if (tid < ranks * HT) {  // this CTA's maximum of head h to rank r
       const int r = tid / HT, h = tid % HT;
       unsigned t = 0;

@@ -137,6 +137,29 @@ def test_rope_append_equals_rope_then_append(new, bs, steady, inter, rot):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("last", [2 ** 31 - 1, -1, 0])
+def test_rope_append_at_the_ends_of_the_positions(last):
+    """Positions that run up to the largest int32, to -1 and through 0, over a shared block."""
+    rng = np.random.default_rng(7)
+    n, bs, hq, hkv, d = 1500, 1024, 2, 1, 128
+    tables, nb = tables_of(rng, [n], bs)
+    qkv = bf16_dev(f32_to_bf16_bits(rng.standard_normal((n, hq + 2 * hkv, d)).astype(np.float32)))
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    pos = i32_dev(np.arange(last - n + 1, last + 1) if last else np.arange(n) - 700)
+    f = torch.tensor(pa.pa_rope_inv_freq(d)[0], dtype=torch.float32, device="cuda")
+    a = [torch.zeros((nb, bs, hkv, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    a += [torch.zeros((nb, hkv), dtype=torch.float32, device="cuda") for _ in range(2)]
+    b = [t.clone() for t in a]
+    q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device="cuda")
+    rest = (i32_dev(tables), i32_dev(np.array([0, n])), i32_dev(np.array([n])), n)
+    pa.pa_rope_store_kvcache_fp8_blockscale(q_out, q, k, v, *a, *rest, pos, f)
+    rk = torch.empty((n, hkv, d), dtype=torch.bfloat16, device="cuda")
+    pa.pa_rope(rk, k, pos, f)
+    pa.pa_store_kvcache_fp8_blockscale(rk, v, *b, *rest)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
 def test_append_bad_lengths_and_blocks_are_reported_and_skipped():
     rng = np.random.default_rng(2)
     hkv, d, bs = 2, 128, 16
