@@ -160,6 +160,30 @@ def test_rope_append_at_the_ends_of_the_positions(last):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("seqs", [0, 2])
+def test_rope_append_of_nothing_still_turns_the_queries(seqs):
+    """Padding tokens only: no sequence, or none with new rows and 0 as the bound of their count."""
+    rng = np.random.default_rng(8)
+    qkv = bf16_dev(f32_to_bf16_bits(rng.standard_normal((5, 8, 128)).astype(np.float32)))
+    q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    kc, ks = pools_of(rng, 3, 16, 2, 128)
+    dev = [u8_dev(kc), u8_dev(kc), f32_dev(ks), f32_dev(ks)]
+    pos, f = i32_dev(np.arange(5)), torch.tensor(pa.pa_rope_inv_freq(128)[0], device="cuda")
+    want, got = (torch.full((5, 4, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pa.pa_rope(want, q, pos, f)
+    lens = i32_dev(np.zeros(seqs)), 0
+    tables = i32_dev(np.ones((seqs, 1)))
+    pa.pa_rope_store_kvcache_fp8_blockscale(got, q, k, v, *dev, tables, i32_dev(np.zeros(seqs + 1)), *lens, pos, f)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    assert np.array_equal(dev[0].cpu().numpy(), kc) and np.array_equal(dev[2].cpu().numpy(), ks)
+    if seqs:  # new rows above the bound are reported
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_store_kvcache_fp8_blockscale(k, v, *dev, tables, i32_dev(np.array([0, 0, 1])),
+                                               i32_dev(np.array([0, 1])), 0)
+        assert e.value.status == 3
+        assert np.array_equal(dev[0].cpu().numpy(), kc)
+
+
 def test_append_bad_lengths_and_blocks_are_reported_and_skipped():
     rng = np.random.default_rng(2)
     hkv, d, bs = 2, 128, 16
