@@ -129,7 +129,7 @@ struct Cfg {
   static constexpr int kOffEpi = round_up(kOffQs + QN * G * 4, 16);
   // heads shared by several epilogue warps meet here when parts are merged
   static constexpr int kOffMerge = round_up(kOffEpi + NO * kEpiBytes, 16);
-  static constexpr int kOffBar = kOffMerge + (G < 4 ? 4 * (HD + 4) * 4 : 0);
+  static constexpr int kOffBar = kOffMerge + (G < 4 ? 4 * HD * 4 : 0);
   static constexpr int kNumBars = 3 * ND + 2 * NK + 2 * NV + 2 * NS + 2 * NP + 2 * QN + 4 * NO + 2;
   static constexpr int kOffMisc = round_up(kOffBar + 8 * kNumBars, 16);
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
@@ -218,6 +218,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float (&v)[N]) {
 // parts in turn with 4 / G - 1 other warps. Lane i reads part i's maximum and sum; the lanes
 // hold 4 output dims each, so a part's row is one 16-byte load per lane, and all of a head's
 // loads are in flight together. Reads bypass L1 (the parts were written by other SMs).
+// The sums' order and roundings do not depend on who arrives last; products are rounded before
+// they are added, so that for two parts either may come first (the epilogue's short way).
 // out non-NULL: the rows' outputs; NULL: the result replaces part 0's record (read and written
 // by the same warps).
 template <int G>
@@ -230,10 +232,8 @@ __device__ __forceinline__ void merge_parts(float* ws_o, float* ws_ml, int cnt, 
   auto slot_of = [&](int i) -> int64_t { return i == 0 ? slot0 : first + i * step; };
 #pragma unroll 1
   for (int h = G >= 4 ? warp4 : warp4 % G; h < G; h += 4) {
-    const int part = lane * S + sub;  // lane i holds the warp's i-th part
-    const bool in = lane < N && part < cnt;
-    const float2 ml = in ? __ldcg(reinterpret_cast<const float2*>(ws_ml) + slot_of(part) * G + h)
-                         : make_float2(-INFINITY, 0.f);
+    const float2 ml = lane < cnt ? __ldcg(reinterpret_cast<const float2*>(ws_ml) + slot_of(lane) * G + h)
+                                 : make_float2(-INFINITY, 0.f);
     float4 o[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -241,45 +241,31 @@ __device__ __forceinline__ void merge_parts(float* ws_o, float* ws_ml, int cnt, 
       if (i * S + sub < cnt)
         o[i] = __ldcg(reinterpret_cast<const float4*>(ws_o + (slot_of(i * S + sub) * G + h) * HD) + lane);
     }
-    float M = warp_max(ml.x);
+    const float M = warp_max(ml.x);
     const float f = M > -INFINITY ? ex2_approx(ml.x - M) : 0.f;
-    float L = ml.y * f;
+    float L = __fmul_rn(ml.y, f);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    for (int off = 16; off > 0; off >>= 1) L = __fadd_rn(L, __shfl_xor_sync(0xffffffffu, L, off));
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i);
-      A.x = fmaf(fi, o[i].x, A.x);
-      A.y = fmaf(fi, o[i].y, A.y);
-      A.z = fmaf(fi, o[i].z, A.z);
-      A.w = fmaf(fi, o[i].w, A.w);
+      const float fi = __shfl_sync(0xffffffffu, f, i * S + sub);
+      A.x = __fadd_rn(A.x, __fmul_rn(fi, o[i].x));
+      A.y = __fadd_rn(A.y, __fmul_rn(fi, o[i].y));
+      A.z = __fadd_rn(A.z, __fmul_rn(fi, o[i].z));
+      A.w = __fadd_rn(A.w, __fmul_rn(fi, o[i].w));
     }
     if constexpr (S > 1) {
       // the warps of a head meet in shared memory; the first one finishes
-      float* mine = buf + warp4 * (HD + 4);
+      float* mine = buf + warp4 * HD;
       reinterpret_cast<float4*>(mine)[lane] = A;
-      if (lane == 0) {
-        mine[HD] = M;
-        mine[HD + 1] = L;
-      }
       named_bar_sync(2, 128);
       if (sub == 0) {
-        float mx = M;
-#pragma unroll
-        for (int w = 1; w < S; ++w) mx = fmaxf(mx, buf[(warp4 + w * G) * (HD + 4) + HD]);
-        const float r = ex2_approx(M - mx);  // the first warp has part 0: M is finite
-        L *= r;
-        A = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
 #pragma unroll
         for (int w = 1; w < S; ++w) {
-          const float* other = buf + (warp4 + w * G) * (HD + 4);
-          const float4 B = reinterpret_cast<const float4*>(other)[lane];
-          const float q = ex2_approx(other[HD] - mx);  // 0 for a warp without parts
-          L = fmaf(q, other[HD + 1], L);
-          A = make_float4(fmaf(q, B.x, A.x), fmaf(q, B.y, A.y), fmaf(q, B.z, A.z), fmaf(q, B.w, A.w));
+          const float4 B = reinterpret_cast<const float4*>(buf + (warp4 + w * G) * HD)[lane];
+          A = make_float4(A.x + B.x, A.y + B.y, A.z + B.z, A.w + B.w);
         }
-        M = mx;
       }
       named_bar_sync(2, 128);  // before the buffer's next use
     }
@@ -1044,45 +1030,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto slot_of = [&](int i) -> int64_t {
         return 2 * (static_cast<int64_t>(it.group0 + i) * p.members + member) + (i == 0 ? 1 : 0);
       };
-      // Are all the other parts there already (a CTA's last item, as a rule: the next CTA took
-      // its rest first)? Then they are merged while this one's last products run, and this
-      // part goes straight into the output.
-      if (leader && !failed && !it.stop && it.nparts > 1) {
-        unsigned long long v = 0;
-        if (it.nparts <= kFan) v = load_acquire(p.counters + 2 * slot_of(0));
-        *last_flag = v == ((p.tag << kCountBits) | static_cast<unsigned>(it.nparts - 1));
-      }
+      // Is the other part of two there already? Then it is read while this one's last products
+      // run, and this one goes straight into the output, with the bits that merge_parts gives
+      // (most split items are in two parts; the code for more of them took 0.8 us longer).
+      if (leader && !failed && !it.stop && it.nparts == 2)
+        *last_flag = load_acquire(p.counters + 2 * slot_of(0)) == ((p.tag << kCountBits) | 1u);
       if (bar_or(2, 128, failed)) break;  // every thread has read the hand-off
       if (leader) mbar_arrive(&epi_empty[b]);
       if (it.stop) break;
-      const bool finish = it.nparts > 1 && *last_flag != 0;
-      float om[G], ol[G], oo[G];  // the other parts
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        om[h] = -INFINITY;
-        ol[h] = 0.f;
-        oo[h] = 0.f;
-      }
+      const bool finish = it.nparts == 2 && *last_flag != 0;
+      float wo[G], po[G];  // this part's weight, the other one's row times its weight
       if (finish) {
-#pragma unroll 1
-        for (int i = 0; i < it.nparts; ++i) {
-          if (i == it.part) continue;
-          const int64_t at = slot_of(i) * G;
-          float2 ml[G];
-          float po[G];
+        const int64_t at = slot_of(it.part ^ 1) * G;
+        float2 ml[G];
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            ml[h] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + at + h);
-            po[h] = __ldcg(p.ws_o + (at + h) * HD + dl);
-          }
+        for (int h = 0; h < G; ++h) {
+          ml[h] = __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + at + h);
+          po[h] = __ldcg(p.ws_o + (at + h) * HD + dl);
+        }
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float mx = fmaxf(om[h], ml[h].x);
-            const float r = ex2_approx(om[h] - mx), f = ex2_approx(ml[h].x - mx);
-            ol[h] = ol[h] * r + ml[h].y * f;
-            oo[h] = oo[h] * r + po[h] * f;
-            om[h] = mx;
-          }
+        for (int h = 0; h < G; ++h) {
+          const float mx = fmaxf(m[h], ml[h].x);
+          const float f = ex2_approx(ml[h].x - mx);
+          wo[h] = ex2_approx(m[h] - mx);
+          L[h] = __fadd_rn(__fmul_rn(L[h], wo[h]), __fmul_rn(ml[h].y, f));
+          po[h] = fmaf(po[h], f, 0.f);  // as in merge_parts, never -0
         }
       }
       failed |= !wait_or_abort(&o_full[b], (k / NO) & 1, p.err, abort_flag, wl);
@@ -1100,18 +1072,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.nparts == 1 || finish) {
         if (finish) {
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float mx = fmaxf(om[h], m[h]);
-            const float r = ex2_approx(om[h] - mx), f = ex2_approx(m[h] - mx);
-            L[h] = ol[h] * r + L[h] * f;
-            o[h] = oo[h] * r + o[h] * f;
-          }
+          for (int h = 0; h < G; ++h) o[h] = __fadd_rn(fmaf(wo[h], o[h], 0.f), po[h]);
           if (leader) *reinterpret_cast<volatile unsigned long long*>(p.counters + 2 * slot_of(0)) = 0ull;
         }
         if (!failed) {
 #pragma unroll
           for (int h = 0; h < G; ++h)
-            p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(__fdividef(o[h], L[h]));
+            p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(o[h] * __fdividef(1.f, L[h]));
         }
       } else {
         const int64_t mine = slot_of(it.part);

@@ -317,6 +317,22 @@ def test_decode_is_deterministic_and_reuses_a_workspace():
     close(first, c.oracle())
 
 
+@pytest.mark.parametrize("g", [1, 4, 16])
+def test_decode_beside_other_work_keeps_its_bits(g):
+    """Another stream's traffic moves the order in which the parts of split items arrive."""
+    c = Case([5000, 700, 3300, 40, 2600, 9000] * 4, 4 * g, 4, 64, seed=g)
+    ws = pa.decode_fp8_blockscale_workspace(24, 4 * g, 4)
+    first = c.gpu(ws)
+    junk, side = torch.zeros(32 << 20, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(30):
+        if i % 3:
+            with torch.cuda.stream(side):
+                junk[:: i % 3 + 1].add_(1.0)
+        assert torch.equal(c.gpu(ws).view(torch.int16), first.view(torch.int16))
+    torch.cuda.synchronize()
+
+
 def test_decode_graphs_share_a_workspace():
     """Two captured calls on one workspace, replayed in turn without clearing it."""
     a, b = Case([5000, 40], 8, 2, 64, seed=21), Case([900] * 9, 8, 2, 16, seed=22)
