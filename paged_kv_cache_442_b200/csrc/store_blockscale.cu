@@ -12,8 +12,8 @@
 // per thread and row (two 16-byte loads). A unit loads its new rows into registers, turns them
 // (K), takes the largest finite magnitude on the bf16 bits, agrees on the scale and writes the
 // codes; rows already in the block are rewritten only when the scale grew. No unit shares a
-// (block, head) with another, so there are no atomics and the result does not depend on the
-// order. HBM-bound: a bf16 row in, half of it out.
+// (block, head) with another, so there are no global atomics and the result does not depend on
+// the order. HBM-bound: a bf16 row in, half of it out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kFewRows = 32;    // new rows of a block that one warp takes
+constexpr int kWindow = 1024;   // sequences whose units are counted at a time
 constexpr int kRowHeads = 8;    // (row, head) pairs a thread keeps in registers (64 registers)
 constexpr int kMaxCluster = 4;  // CTAs that share a block of 1024 rows
 constexpr int kQTokens = 2;        // tokens of a CTA that turns queries
@@ -53,14 +54,14 @@ struct AppendParams {
   int num_seqs;
   int num_tokens;
   int max_new;
-  int span;  // blocks that max_new consecutive positions can reach
   int max_blocks;
   int num_blocks;
   int bs_log2;
   int num_q_heads;
   int num_kv_heads;
   int q_ctas;
-  int cluster;  // CTAs per block (append_many_kernel)
+  int span;     // blocks that max_new consecutive positions can reach
+  int cluster;  // CTAs per block of many rows
   unsigned* err;
 };
 
@@ -183,38 +184,53 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p,
   }
 }
 
-// The new rows of one (sequence, j-th block they reach): `rows` rows from offset r0 of the
-// block, tokens tok0 ... false: nothing to do (or bad lengths, which `report` records).
+// A sequence's new rows: n rows from token `begin` on, the last one at position ctx - 1.
+struct Seq {
+  int begin, n, ctx;
+};
+
+// Lengths of sequence s; n = 0 (and an error, if `report`) when they do not fit.
+__device__ __forceinline__ Seq seq_of(const AppendParams& p, int s, bool report) {
+  Seq q;
+  q.begin = __ldg(p.cu_seqlens + s);
+  const int end = __ldg(p.cu_seqlens + s + 1);
+  q.ctx = __ldg(p.context_lens + s);
+  q.n = end - q.begin;
+  if (q.begin < 0 || end < q.begin || end > p.num_tokens || q.n > p.max_new || q.ctx < q.n ||
+      static_cast<int64_t>(q.ctx) > (static_cast<int64_t>(p.max_blocks) << p.bs_log2)) {
+    if (report) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+    q.n = 0;
+  }
+  return q;
+}
+
+// Blocks that a sequence's new rows reach.
+__device__ __forceinline__ int blocks_of(const AppendParams& p, const Seq& q) {
+  return q.n ? ((q.ctx - 1) >> p.bs_log2) - ((q.ctx - q.n) >> p.bs_log2) + 1 : 0;
+}
+
+// The rows of sequence s that go to the j-th block they reach: `rows` rows from offset r0 of
+// the block, tokens tok0 ...
 struct Span {
   int id;  // physical block, unchecked
   int rows, r0;
   int64_t tok0;
 };
 
-__device__ __forceinline__ bool find_span(const AppendParams& p, int s, int j, bool report,
-                                          Span& u) {
-  const int begin = __ldg(p.cu_seqlens + s), end = __ldg(p.cu_seqlens + s + 1);
-  const int ctx = __ldg(p.context_lens + s);
-  const int n = end - begin;
-  if (begin < 0 || n < 0 || end > p.num_tokens || n > p.max_new || ctx < n ||
-      static_cast<int64_t>(ctx) > (static_cast<int64_t>(p.max_blocks) << p.bs_log2)) {
-    if (report) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
-    return false;
-  }
-  if (n == 0) return false;
-  const int pos0 = ctx - n;
+__device__ __forceinline__ Span span_of(const AppendParams& p, const Seq& q, int s, int j) {
+  const int pos0 = q.ctx - q.n;
   const int blk = (pos0 >> p.bs_log2) + j;
   const int64_t start = static_cast<int64_t>(blk) << p.bs_log2;
   const int64_t stop = start + (1ll << p.bs_log2);
-  const int lo = start > pos0 ? static_cast<int>(min(start, static_cast<int64_t>(ctx))) : pos0;
-  const int hi = stop < ctx ? static_cast<int>(stop) : ctx;
-  if (lo >= hi) return false;
+  const int lo = start > pos0 ? static_cast<int>(start) : pos0;
+  const int hi = stop < q.ctx ? static_cast<int>(stop) : q.ctx;
+  Span u;
   // read while the rows' loads are on their way; checked by the caller after issuing them
   u.id = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks + blk);
   u.rows = hi - lo;
   u.r0 = lo & ((1 << p.bs_log2) - 1);
-  u.tok0 = begin + (lo - pos0);
-  return true;
+  u.tok0 = q.begin + (lo - pos0);
+  return u;
 }
 
 // Largest finite magnitude (bits) of N vectors.
@@ -258,8 +274,11 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const AppendParams
   const int grp = tid % NG, hl = tid / NG;
   const int2 at = rope_vectors(grp, p.rope);
   const bool in_rot = grp < (p.rope.rot_dim >> 4);
+  Seq seq{};
+  if (i < p.num_seqs) seq = seq_of(p, i, tid == 0);
+  const bool stored = seq.n > 0;
   Span u{};
-  const bool stored = i < p.num_seqs && find_span(p, i, 0, tid == 0, u);
+  if (stored) u = span_of(p, seq, i, 0);
   const int q_heads = i < p.num_tokens ? p.num_q_heads : 0;
   const int kv_heads = stored ? 2 * p.num_kv_heads : 0;  // K heads, then V heads
   const int heads = q_heads + kv_heads;
@@ -351,31 +370,13 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const AppendParams
   }
 }
 
-// Few new rows per block (short chunks; blocks of 16 and 32): a warp per (sequence, block,
-// K or V, head), eight to a CTA.
-template <int D>
-__global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams p) {
+// The new rows of a block that takes at most ROWS, of head g of K or V, by one warp.
+template <int D, int ROWS>
+__device__ __forceinline__ void append_few(const AppendParams& p, const Span& u, bool is_v, int g,
+                                           int lane) {
   constexpr int NG = D / 16;         // threads per row
   constexpr int RL = 32 / NG;        // rows side by side
-  constexpr int RT = kFewRows / RL;  // rows a thread keeps in registers (8 at 128 dims)
-  __shared__ RopeTable<kQTokens, D / 2> table;
-  if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {
-    turn_queries<D>(p, table);
-    return;
-  }
-  const int lane = threadIdx.x & 31;
-  const int64_t unit =
-      static_cast<int64_t>(blockIdx.x - p.q_ctas) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t per_seq = static_cast<int64_t>(p.span) * 2 * p.num_kv_heads;
-  if (unit >= per_seq * p.num_seqs) return;
-  const int s = static_cast<int>(unit / per_seq);
-  int rest = static_cast<int>(unit - s * per_seq);
-  const int g = rest % p.num_kv_heads;
-  rest /= p.num_kv_heads;
-  const bool is_v = rest & 1;
-  Span u;
-  if (!find_span(p, s, rest >> 1, lane == 0, u)) return;
-
+  constexpr int RT = ROWS / RL;      // rows a thread keeps in registers
   const int grp = lane % NG, rl = lane / NG;
   const int2 at = rope_vectors(grp, p.rope);
   const bool turned = !is_v && grp < (p.rope.rot_dim >> 4);
@@ -444,40 +445,25 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams
 // Turns: two tables in shared memory, the high and the low factor (rope.cuh) of the CTA's
 // consecutive positions; a row whose position does not follow is turned by the series.
 template <int D, int HT>
-__global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendParams p) {
-  constexpr int NG = D / 16;
-  constexpr int RL = kThreads / NG;      // rows side by side
-  constexpr int RT = kRowHeads / HT;     // rows per thread
-  constexpr int CAP = RL * RT;           // rows of a CTA
-  constexpr int HIGH = CAP / kRopeLow + 1;
-  __shared__ union {
-    RopeTable<kQTokens, D / 2> queries;
-    struct {
-      RopeTable<HIGH, D / 2> high;
-      RopeTable<kRopeLow, D / 2> low;
-    } k;
-  } tables;
-  __shared__ unsigned warp_top[kThreads / 32][HT];
-  __shared__ unsigned cta_top[kMaxCluster][HT];
-  if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {  // whole clusters
-    turn_queries<D>(p, tables.queries);
-    return;
-  }
+struct ManyShared {
+  static constexpr int RL = kThreads / (D / 16);  // rows side by side
+  static constexpr int RT = kRowHeads / HT;       // rows per thread
+  static constexpr int CAP = RL * RT;             // rows of a CTA
+  static constexpr int HIGH = CAP / kRopeLow + 1;
+  RopeTable<HIGH, D / 2> high;
+  RopeTable<kRopeLow, D / 2> low;
+  unsigned warp_top[kThreads / 32][HT];
+  unsigned cta_top[kMaxCluster][HT];
+};
+
+template <int D, int HT>
+__device__ __forceinline__ void append_many(const AppendParams& p, const Span& u, bool is_v, int g,
+                                            ManyShared<D, HT>& tables) {
+  using M = ManyShared<D, HT>;
+  constexpr int NG = D / 16, RL = M::RL, RT = M::RT, CAP = M::CAP, HIGH = M::HIGH;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = p.cluster, rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x;
-  const int64_t unit = (blockIdx.x - p.q_ctas) / ranks;
-  const int hgroups = p.num_kv_heads / HT;
-  const int64_t per_seq = static_cast<int64_t>(p.span) * 2 * hgroups;
-  const int s = static_cast<int>(unit / per_seq);
-  int rest = static_cast<int>(unit - s * per_seq);
-  const int g = rest % hgroups * HT;
-  rest /= hgroups;
-  const bool is_v = rest & 1;
-  Span u;
-  // (every return up to the exchange is taken by the whole cluster)
-  if (!find_span(p, s, rest >> 1, tid == 0 && rank == 0, u)) return;
-
   const int grp = tid % NG, rl = tid / NG;
   const int2 at = rope_vectors(grp, p.rope);
   const bool turned = !is_v && grp < (p.rope.rot_dim >> 4);
@@ -499,11 +485,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
       }
     }
   }
-  if (u.id < 0 || u.id >= p.num_blocks) {
+  if (u.id < 0 || u.id >= p.num_blocks) {  // so for the whole cluster
     if (tid == 0 && rank == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
     return;
   }
-  if (ranks > 1) cluster.barrier_arrive();  // this CTA runs: its shared memory may be written
+  if (ranks > 1) cluster.barrier_arrive();  // this CTA is here: its shared memory may be written
   const int64_t scale_row = static_cast<int64_t>(u.id) * p.num_kv_heads + g;
   float* scales = is_v ? p.v_scales : p.k_scales;
   float old[HT];
@@ -519,9 +505,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
     const int apart = kThreads / half, row0 = tid / half, f = tid - row0 * half;
     if (row0 < apart) {
       const unsigned long long rate = rope_rate(__ldg(p.rope.inv_freq + f));
-      for (int row = row0; row < kRopeLow; row += apart) tables.k.low.put(row, f, rope_low(row, rate));
+      for (int row = row0; row < kRopeLow; row += apart) tables.low.put(row, f, rope_low(row, rate));
       for (int row = row0; row < HIGH; row += apart)
-        tables.k.high.put(row, f, rope_high(static_cast<int>(base + row * kRopeLow), rate, p.rope.amplitude));
+        tables.high.put(row, f, rope_high(static_cast<int>(base + row * kRopeLow), rate, p.rope.amplitude));
     }
     __syncthreads();
     if (turned) {
@@ -532,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
         const unsigned high = (static_cast<unsigned>(at_pos) - base) / kRopeLow;
         RopeTurns cs;
         if (high < HIGH) {
-          cs = rope_product(tables.k.high.group(high, grp),
-                            tables.k.low.group(at_pos & (kRopeLow - 1), grp));
+          cs = rope_product(tables.high.group(high, grp),
+                            tables.low.group(at_pos & (kRopeLow - 1), grp));
         } else {
 #pragma unroll 1
           for (int e = 0; e < 8; ++e) {
@@ -559,17 +545,17 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
       bh[i] = b[i][h];
     }
     const unsigned t = __reduce_max_sync(0xffffffffu, top_of(ah, bh));
-    if ((tid & 31) == 0) warp_top[tid >> 5][h] = t;
+    if ((tid & 31) == 0) tables.warp_top[tid >> 5][h] = t;
   }
   __syncthreads();
   if (ranks > 1) {
-    cluster.barrier_wait();  // every CTA of the cluster runs
+    cluster.barrier_wait();
     if (tid < ranks * HT) {  // this CTA's maximum of head h to rank r
       const int r = tid / HT, h = tid % HT;
       unsigned t = 0;
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) t = max(t, warp_top[w][h]);
-      *cluster.map_shared_rank(&cta_top[rank][h], r) = t;
+      for (int w = 0; w < kThreads / 32; ++w) t = max(t, tables.warp_top[w][h]);
+      *cluster.map_shared_rank(&tables.cta_top[rank][h], r) = t;
     }
     cluster.sync();
   }
@@ -581,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
   for (int h = 0; h < HT; ++h) {
     unsigned t = 0;
     if (ranks > 1) {
-      for (int r = 0; r < ranks; ++r) t = max(t, cta_top[r][h]);
+      for (int r = 0; r < ranks; ++r) t = max(t, tables.cta_top[r][h]);
     } else {
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) t = max(t, warp_top[w][h]);
+      for (int w = 0; w < kThreads / 32; ++w) t = max(t, tables.warp_top[w][h]);
     }
     const float need = exp2_int(scale_exponent(t));
     const float scale = old[h] >= need ? old[h] : need;  // old is 0 for a block that starts here
@@ -605,15 +591,163 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
   }
 }
 
+// The units as the host bounds them: max_new rows' blocks for every sequence, of which those
+// past a sequence's own have nothing to do. Few rows a block: a warp per unit.
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams p) {
+  __shared__ RopeTable<kQTokens, D / 2> table;
+  if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {
+    turn_queries<D>(p, table);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const int64_t unit =
+      static_cast<int64_t>(blockIdx.x - p.q_ctas) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t per_seq = static_cast<int64_t>(p.span) * 2 * p.num_kv_heads;
+  if (unit >= per_seq * p.num_seqs) return;
+  const int s = static_cast<int>(unit / per_seq);
+  int rest = static_cast<int>(unit - s * per_seq);
+  const int g = rest % p.num_kv_heads;
+  rest /= p.num_kv_heads;
+  const Seq q = seq_of(p, s, lane == 0);
+  if ((rest >> 1) < blocks_of(p, q))
+    append_few<D, kFewRows>(p, span_of(p, q, s, rest >> 1), rest & 1, g, lane);
+}
+
+// The same with a CTA or a cluster per unit of HT heads.
 template <int D, int HT>
-cudaError_t launch_many(AppendParams p, int rows, cudaStream_t stream) {
-  constexpr int CAP = kThreads / (D / 16) * (kRowHeads / HT);
-  p.cluster = 1;
-  while (p.cluster * CAP < rows) p.cluster *= 2;
-  static_assert(kMaxCluster * (kThreads / (D / 16)) * kRowHeads >= 1024, "the largest block");
-  p.q_ctas = (p.q_ctas + p.cluster - 1) / p.cluster * p.cluster;
-  const int64_t grid = p.q_ctas + static_cast<int64_t>(p.num_seqs) * p.span * 2 *
-                                      (p.num_kv_heads / HT) * p.cluster;
+__global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendParams p) {
+  __shared__ union {
+    RopeTable<kQTokens, D / 2> queries;
+    ManyShared<D, HT> many;
+  } sm;
+  if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {  // whole clusters
+    turn_queries<D>(p, sm.queries);
+    return;
+  }
+  const int64_t unit = (blockIdx.x - p.q_ctas) / p.cluster;
+  const int hgroups = p.num_kv_heads / HT;
+  const int64_t per_seq = static_cast<int64_t>(p.span) * 2 * hgroups;
+  const int s = static_cast<int>(unit / per_seq);
+  int rest = static_cast<int>(unit - s * per_seq);
+  const int g = rest % hgroups * HT;
+  rest /= hgroups;
+  const Seq q = seq_of(p, s, threadIdx.x == 0);
+  if ((rest >> 1) < blocks_of(p, q))
+    append_many<D, HT>(p, span_of(p, q, s, rest >> 1), rest & 1, g, sm.many);
+}
+
+// Batches whose sequences' new rows differ much, one long chunk beside many single tokens: most
+// of the units above would have nothing to do. Here every CTA (or cluster) counts the
+// sequences' own units, a scan over 1024 sequences at a time, and the CTAs that fit the GPU take
+// them in turn; in a block that takes few rows, eight heads are one unit, a warp each (MANY:
+// some take more). The scan costs 2 - 3 us.
+template <int D, bool MANY>
+__global__ void __launch_bounds__(kThreads, 2) append_ragged_kernel(const AppendParams p) {
+  constexpr int kEach = kWindow / kThreads;
+  constexpr int FEW = MANY ? kFewRows / 2 : kFewRows;  // beside many rows' registers, half as many
+  __shared__ union {
+    RopeTable<kQTokens, D / 2> queries;
+    ManyShared<D, 1> many;
+  } sm;
+  __shared__ long long first_unit[kWindow];
+  __shared__ Seq seqs[kWindow];
+  __shared__ long long warp_sum[kThreads / 32];
+  if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {  // whole clusters
+    turn_queries<D>(p, sm.queries);
+    return;
+  }
+  const int ranks = p.cluster, rank = blockIdx.x % ranks;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int few_units = (2 * p.num_kv_heads + 8 * ranks - 1) / (8 * ranks);  // of a block
+  const int many_units = 2 * p.num_kv_heads;
+  // a sequence's blocks, and whether its first and its last one take few rows
+  struct Blocks {
+    int n;
+    bool first, last;
+  };
+  auto counted = [&](const Seq& q) {
+    const int mask = (1 << p.bs_log2) - 1;
+    const int left = mask + 1 - ((q.ctx - q.n) & mask);  // rows to the first block's end
+    Blocks b;
+    b.n = blocks_of(p, q);
+    b.first = b.n > 0 && min(q.n, left) <= FEW;
+    b.last = b.n > 1 && ((q.ctx - 1) & mask) < FEW;
+    return b;
+  };
+  const int stride = (gridDim.x - p.q_ctas) / ranks;
+  int64_t unit = (blockIdx.x - p.q_ctas) / ranks;  // counted from the window's first
+  for (int s0 = 0; s0 < p.num_seqs; s0 += kWindow) {
+    const int count = min(kWindow, p.num_seqs - s0);
+    long long mine[kEach], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = tid * kEach + e;
+      mine[e] = sum;
+      if (i < count) {
+        const Seq q = seq_of(p, s0 + i, blockIdx.x == static_cast<unsigned>(p.q_ctas));
+        seqs[i] = q;
+        const Blocks b = counted(q);
+        const int few = MANY ? b.first + b.last : b.n;
+        sum += static_cast<long long>(few) * few_units + static_cast<long long>(b.n - few) * many_units;
+      }
+    }
+    long long upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += up;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    long long before = upto - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (tid * kEach + e < count) first_unit[tid * kEach + e] = before + mine[e];
+    __syncthreads();
+    for (; unit < total; unit += stride) {
+      int i = 0;  // the last sequence whose first unit is not after this one
+      for (int n = count; n > 1;) {
+        const int half = n >> 1;
+        if (first_unit[i + half] <= unit) i += half, n -= half;
+        else n = half;
+      }
+      const Seq q = seqs[i];
+      const Blocks b = counted(q);
+      // a sequence's units: of its blocks with many rows, then of those with few
+      int64_t at = unit - first_unit[i];
+      if constexpr (MANY) {
+        const int64_t many = static_cast<int64_t>(b.n - b.first - b.last) * many_units;
+        if (at < many) {
+          const int j = static_cast<int>(at / many_units), rest = static_cast<int>(at - j * static_cast<int64_t>(many_units));
+          const bool is_v = rest >= p.num_kv_heads;
+          __syncthreads();  // the tables are free
+          append_many<D, 1>(p, span_of(p, q, s0 + i, j + b.first), is_v,
+                            is_v ? rest - p.num_kv_heads : rest, sm.many);
+          continue;
+        }
+        at -= many;
+      }
+      const int f = static_cast<int>(at / few_units);
+      const int pair = (static_cast<int>(at - f * static_cast<int64_t>(few_units)) * ranks + rank) * (kThreads / 32) + warp;
+      if (pair < 2 * p.num_kv_heads) {
+        const bool is_v = pair >= p.num_kv_heads;
+        append_few<D, FEW>(p, span_of(p, q, s0 + i, !MANY ? f : f == 0 && b.first ? 0 : b.n - 1), is_v,
+                           is_v ? pair - p.num_kv_heads : pair, lane);
+      }
+    }
+    unit -= total;
+    __syncthreads();  // before the next window's lists
+  }
+}
+
+template <class Kernel>
+cudaError_t launch_clusters(Kernel kernel, const AppendParams& p, int64_t grid, cudaStream_t stream) {
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -625,8 +759,8 @@ cudaError_t launch_many(AppendParams p, int rows, cudaStream_t stream) {
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_many_kernel<D, HT>, p);
+  cfg.numAttrs = p.cluster > 1;  // clusters of one CTA took longer (512 tokens in blocks of 16: 10.7 us against 8.8)
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int D>
@@ -641,17 +775,31 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
     append_one_kernel<D><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
   }
-  if (rows <= kFewRows) {
-    const int64_t units = static_cast<int64_t>(p.num_seqs) * p.span * 2 * p.num_kv_heads;
-    const int64_t grid = p.q_ctas + (units + kThreads / 32 - 1) / (kThreads / 32);
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    append_few_kernel<D><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+  constexpr int CAP = ManyShared<D, 1>::CAP;  // rows of one head that a CTA holds
+  static_assert(kMaxCluster * CAP >= 1024, "the largest block");
+  const int ht = p.num_kv_heads % 4 == 0 && rows <= CAP / 4 ? 4 : p.num_kv_heads % 2 == 0 && rows <= CAP / 2 ? 2 : 1;
+  const bool few = rows <= kFewRows;
+  while (!few && p.cluster * CAP < rows * ht) p.cluster *= 2;
+  p.q_ctas = (p.q_ctas + p.cluster - 1) / p.cluster * p.cluster;
+  const int64_t spans = static_cast<int64_t>(p.num_seqs) * p.span;
+  const int64_t ctas = few ? (spans * 2 * p.num_kv_heads + kThreads / 32 - 1) / (kThreads / 32)
+                           : spans * 2 * (p.num_kv_heads / ht) * p.cluster;
+  // Counting pays beyond four waves of CTAs, when the blocks would hold an eighth of the most
+  // rows on average. Without / with it, us (32 q and 8 kv heads): 255 single tokens and a chunk
+  // of 8192, blocks of 256, 400 / 59; 63 and 2048 47 / 21; 15 and 2048 24.1 / 20.5; 63 and 512,
+  // blocks of 16, 20.2 / 13.9; on the other side 63 and 40, blocks of 64 (1.7 waves) 7.5 / 8.5, 98
+  // ragged of up to 45 (a quarter full) 15.2 / 20.5, 64 even chunks of 256 82 / 97.
+  const int64_t sms = sm_count();
+  if (ctas > 8 * sms && static_cast<int64_t>(p.num_tokens) * 8 < spans * rows) {
+    // as many CTAs as are resident
+    const int64_t grid = p.q_ctas + 2 * sms / p.cluster * p.cluster;
+    return few ? launch_clusters(append_ragged_kernel<D, false>, p, grid, stream)
+               : launch_clusters(append_ragged_kernel<D, true>, p, grid, stream);
   }
-  constexpr int CAP = kThreads / (D / 16) * kRowHeads;  // rows of one head that a CTA holds
-  if (p.num_kv_heads % 4 == 0 && rows <= CAP / 4) return launch_many<D, 4>(p, rows, stream);
-  if (p.num_kv_heads % 2 == 0 && rows <= CAP / 2) return launch_many<D, 2>(p, rows, stream);
-  return launch_many<D, 1>(p, rows, stream);
+  if (few) return launch_clusters(append_few_kernel<D>, p, p.q_ctas + ctas, stream);
+  if (ht == 4) return launch_clusters(append_many_kernel<D, 4>, p, p.q_ctas + ctas, stream);
+  if (ht == 2) return launch_clusters(append_many_kernel<D, 2>, p, p.q_ctas + ctas, stream);
+  return launch_clusters(append_many_kernel<D, 1>, p, p.q_ctas + ctas, stream);
 }
 
 }  // namespace

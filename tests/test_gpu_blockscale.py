@@ -82,6 +82,12 @@ def same_codes(got, want):
     (2, 64, 128, [2500, 77], [100, 127]),
     (3, 128, 256, [3000], [1]),
     (2, 128, 1024, [1500, 900], [700, 0]),                    # blocks read twice
+    # one long chunk beside many short ones
+    (8, 128, 16, [1] * 30 + [700] + [2, 0, 17, 5] * 8, list(range(63))),
+    (8, 128, 64, [1] * 20 + [33, 17, 16, 0] + [600] + [1] * 20, list(range(40, 85))),
+    (3, 128, 1024, [1] * 25 + [900] + [40, 3, 16] * 8, [1000] * 20 + list(range(30))),
+    (4, 64, 256, [1] * 40 + [1300, 300] + [1, 2] * 10, list(range(200, 262))),
+    (1, 64, 64, [1] * 1100 + [0] * 5 + [300] + [1, 2, 3] * 100, [3] * 1406),   # two windows of sequences
 ])
 def test_append_matches_the_oracle_bit_for_bit(hkv, d, bs, new, old):
     rng = np.random.default_rng(bs + d + sum(new))
@@ -105,7 +111,9 @@ def test_append_matches_the_oracle_bit_for_bit(hkv, d, bs, new, old):
 @pytest.mark.parametrize("inter,rot", [(False, 128), (True, 64), (False, 16), (True, 48), (False, 0)])
 @pytest.mark.parametrize("new,bs,steady", [([1, 1, 1], 256, True), ([1, 0, 1, 1], 64, True), ([70, 3], 64, False),
                                            ([70, 3], 64, True), ([300, 129, 1000], 256, True), ([5, 20], 32, True),
-                                           ([1024 + 700], 1024, True), ([400], 512, False)])
+                                           ([1024 + 700], 1024, True), ([400], 512, False),
+                                           ([1] * 150 + [900] + [20, 1, 2] * 9, 256, True),
+                                           ([3] * 200 + [600], 16, True)])
 def test_rope_append_equals_rope_then_append(new, bs, steady, inter, rot):
     """steady: positions follow one another, as a rule; else they are anywhere."""
     rng = np.random.default_rng(rot + bs)
@@ -212,6 +220,31 @@ def test_append_bad_lengths_and_blocks_are_reported_and_skipped():
         assert np.array_equal(got, exp)
     got = run(good, [0, 2, 5, 6], [2, 3, 1], 2)                                     # above max_q_len
     assert np.array_equal(got[2], kc[2]) and np.array_equal(got[1], want[1])
+
+
+def test_append_of_a_ragged_batch_reports_what_it_skips():
+    rng = np.random.default_rng(12)
+    new = np.array([1] * 40 + [600] + [2] * 20)
+    hkv, d, bs, n, old = 8, 128, 64, len(new), 5
+    ctx = new + old
+    tables, nb = tables_of(rng, ctx, bs)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    k = bf16_dev(f32_to_bf16_bits(rng.standard_normal((int(cu[-1]), hkv, d)).astype(np.float32)))
+    kc, ks = pools_of(rng, nb, bs, hkv, d)
+    want = fp8_block.append(kc, ks, to_bits(k), tables, cu, ctx)
+    skipped, bad_block = (3, 45), 40
+    ctx2, tables2 = ctx.copy(), tables.copy()
+    ctx2[3], ctx2[45] = 0, bs * tables.shape[1] + 1     # fewer than the new rows; past the table
+    tables2[bad_block, 2] = nb                          # one block of the chunk
+    t = [u8_dev(kc), u8_dev(kc), f32_dev(ks), f32_dev(ks)]
+    with pytest.raises(pa.PAError) as e:
+        pa.pa_store_kvcache_fp8_blockscale(k, k, *t, i32_dev(tables2), i32_dev(cu), i32_dev(ctx2), 600)
+    assert e.value.status == 3
+    codes, scales = want[0].copy(), want[1].copy()
+    left = [int(tables[s, 0]) for s in skipped] + [int(tables[bad_block, 2])]
+    codes[left], scales[left] = kc[left], ks[left]
+    for got_c, got_s in ((t[0], t[2]), (t[1], t[3])):
+        assert np.array_equal(got_c.cpu().numpy(), codes) and np.array_equal(got_s.cpu().numpy(), scales)
 
 
 # ------------------------------------------------------------------------------ decode
