@@ -86,6 +86,9 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeStorePar
   constexpr int HL = kThreads / (NG * TB);     // heads walked side by side
   __shared__ RopeTable<TB, D / 2> table;
   const int tid = threadIdx.x;
+  // a kernel launched behind this one that does not read its outputs may start when every CTA
+  // of this one has (the append of the same step's keys and values)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int g = tid % NG;
   const int tk = (tid / NG) % TB;
   const int hl = tid / (NG * TB);

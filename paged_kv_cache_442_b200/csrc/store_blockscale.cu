@@ -60,6 +60,7 @@ struct AppendParams {
   int num_q_heads;
   int num_kv_heads;
   int q_ctas;
+  bool behind_queries;  // may start beside the queries' kernel, whose outputs it does not read
   int span;     // blocks that max_new consecutive positions can reach
   int cluster;  // CTAs per block of many rows
   unsigned* err;
@@ -614,8 +615,9 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams
     append_few<D, kFewRows>(p, span_of(p, q, s, rest >> 1), rest & 1, g, lane);
 }
 
-// The same with a CTA or a cluster per unit of HT heads.
-template <int D, int HT>
+// The same with a CTA or a cluster per unit of HT heads. (BEHIND at compile time: the wait in the
+// code took calls of a few tokens 0.15 us.)
+template <int D, int HT, bool BEHIND>
 __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendParams p) {
   __shared__ union {
     RopeTable<kQTokens, D / 2> queries;
@@ -635,6 +637,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
   const Seq q = seq_of(p, s, threadIdx.x == 0);
   if ((rest >> 1) < blocks_of(p, q))
     append_many<D, HT>(p, span_of(p, q, s, rest >> 1), rest & 1, g, sm.many);
+  // complete, for what follows in the stream, only once the queries' kernel is
+  if (BEHIND && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Batches whose sequences' new rows differ much, one long chunk beside many single tokens: most
@@ -747,19 +751,26 @@ __global__ void __launch_bounds__(kThreads, 2) append_ragged_kernel(const Append
 }
 
 template <class Kernel>
-cudaError_t launch_clusters(Kernel kernel, const AppendParams& p, int64_t grid, cudaStream_t stream) {
+cudaError_t launch(Kernel kernel, const AppendParams& p, int64_t grid, cudaStream_t stream) {
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(p.cluster);
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.cluster > 1;  // clusters of one CTA took longer (512 tokens in blocks of 16: 10.7 us against 8.8)
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (p.cluster > 1) {  // clusters of one CTA took longer (512 tokens in blocks of 16: 10.7 us against 8.8)
+    cudaLaunchAttribute& c = attr[cfg.numAttrs++];
+    c.id = cudaLaunchAttributeClusterDimension;
+    c.val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    c.val.clusterDim.y = 1;
+    c.val.clusterDim.z = 1;
+  }
+  if (p.behind_queries) {
+    cudaLaunchAttribute& c = attr[cfg.numAttrs++];
+    c.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    c.val.programmaticStreamSerializationAllowed = 1;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -771,14 +782,15 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
   p.q_ctas = p.num_q_heads > 0 ? (p.num_tokens + kQTokens - 1) / kQTokens : 0;
   p.cluster = 1;
   if (p.max_new == 1) {
+    p.behind_queries = false;
     const int grid = p.num_q_heads > 0 && p.num_tokens > p.num_seqs ? p.num_tokens : p.num_seqs;
-    append_one_kernel<D><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch(append_one_kernel<D>, p, grid, stream);
   }
   constexpr int CAP = ManyShared<D, 1>::CAP;  // rows of one head that a CTA holds
   static_assert(kMaxCluster * CAP >= 1024, "the largest block");
   const int ht = p.num_kv_heads % 4 == 0 && rows <= CAP / 4 ? 4 : p.num_kv_heads % 2 == 0 && rows <= CAP / 2 ? 2 : 1;
   const bool few = rows <= kFewRows;
+  if (few) p.behind_queries = false;
   while (!few && p.cluster * CAP < rows * ht) p.cluster *= 2;
   p.q_ctas = (p.q_ctas + p.cluster - 1) / p.cluster * p.cluster;
   const int64_t spans = static_cast<int64_t>(p.num_seqs) * p.span;
@@ -791,15 +803,20 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
   // ragged of up to 45 (a quarter full) 15.2 / 20.5, 64 even chunks of 256 82 / 97.
   const int64_t sms = sm_count();
   if (ctas > 8 * sms && static_cast<int64_t>(p.num_tokens) * 8 < spans * rows) {
-    // as many CTAs as are resident
+    // as many CTAs as are resident (not beside the queries' kernel: 63 and 2048 took 22.5 us)
+    p.behind_queries = false;
     const int64_t grid = p.q_ctas + 2 * sms / p.cluster * p.cluster;
-    return few ? launch_clusters(append_ragged_kernel<D, false>, p, grid, stream)
-               : launch_clusters(append_ragged_kernel<D, true>, p, grid, stream);
+    return few ? launch(append_ragged_kernel<D, false>, p, grid, stream)
+               : launch(append_ragged_kernel<D, true>, p, grid, stream);
   }
-  if (few) return launch_clusters(append_few_kernel<D>, p, p.q_ctas + ctas, stream);
-  if (ht == 4) return launch_clusters(append_many_kernel<D, 4>, p, p.q_ctas + ctas, stream);
-  if (ht == 2) return launch_clusters(append_many_kernel<D, 2>, p, p.q_ctas + ctas, stream);
-  return launch_clusters(append_many_kernel<D, 1>, p, p.q_ctas + ctas, stream);
+  if (few) return launch(append_few_kernel<D>, p, p.q_ctas + ctas, stream);
+  auto many = [&](auto plain, auto behind) {
+    return p.behind_queries ? launch(behind, p, p.q_ctas + ctas, stream)
+                            : launch(plain, p, p.q_ctas + ctas, stream);
+  };
+  if (ht == 4) return many(append_many_kernel<D, 4, false>, append_many_kernel<D, 4, true>);
+  if (ht == 2) return many(append_many_kernel<D, 2, false>, append_many_kernel<D, 2, true>);
+  return many(append_many_kernel<D, 1, false>, append_many_kernel<D, 1, true>);
 }
 
 }  // namespace
@@ -835,8 +852,10 @@ cudaError_t launch_append_blockscale(const AppendLaunch& a, cudaStream_t stream)
   p.num_kv_heads = a.cache.num_kv_heads;
   p.err = device_error_word();
   // Few tokens: one launch, whose first CTAs turn the queries. Many: the queries' own kernel
-  // (64 registers against the units' 128, so twice the warps stream them).
+  // (64 registers against the units' 128, so twice the warps stream them), beside whose last
+  // CTAs the units of many rows may start (16384 tokens 82.7 -> 80.0 us, 1147 16.6 -> 15.6).
   const bool q_here = a.num_tokens <= 8 * sm_count();
+  p.behind_queries = !q_here && a.num_q_heads > 0;
   if (!q_here && a.num_q_heads > 0) {
     RopeStoreLaunch q{};
     q.q_out = a.q_out;

@@ -222,6 +222,54 @@ def test_append_bad_lengths_and_blocks_are_reported_and_skipped():
     assert np.array_equal(got[2], kc[2]) and np.array_equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("bs", [64, 512])
+def test_a_long_append_is_complete_for_what_follows(bs):
+    """The queries and the rows of many tokens are two launches that may overlap; what comes
+    before and after them in the stream must not. Captured and replayed."""
+    rng = np.random.default_rng(bs)
+    n, hq, hkv, d = 2600, 16, 4, 128
+    tables, nb = tables_of(rng, [n], bs)
+    qkv = bf16_dev(f32_to_bf16_bits(rng.standard_normal((n, hq + 2 * hkv, d)).astype(np.float32)))
+    work, seen_q = torch.empty_like(qkv), torch.empty((n, hq, d), dtype=torch.bfloat16, device="cuda")
+    q_out = torch.empty_like(seen_q)
+    pools = [torch.zeros((nb, bs, hkv, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pools += [torch.zeros((nb, hkv), dtype=torch.float32, device="cuda") for _ in range(2)]
+    seen = [torch.empty_like(t) for t in pools]
+    rest = (i32_dev(tables), i32_dev(np.array([0, n])), i32_dev(np.array([n])), n)
+    pos, f = i32_dev(np.arange(n)), torch.tensor(pa.pa_rope_inv_freq(d)[0], device="cuda")
+
+    def step():
+        work.copy_(qkv)
+        pa.pa_rope_store_kvcache_fp8_blockscale(q_out, work[:, :hq], work[:, hq:hq + hkv], work[:, hq + hkv:],
+                                                *pools, *rest, pos, f)
+        for a, b in zip([seen_q] + seen, [q_out] + pools):
+            a.copy_(b)
+            b.zero_()
+        work.zero_()
+
+    step()
+    want = [t.clone() for t in [seen_q] + seen]
+    rq = torch.empty_like(q_out)
+    pa.pa_rope(rq, qkv[:, :hq], pos, f)
+    assert torch.equal(rq.view(torch.int16), want[0].view(torch.int16)) and all(t.any() for t in want)
+    pa.pa_set_debug_checks(False)
+    try:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            for _ in range(3):
+                step()
+        for _ in range(10):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip([seen_q] + seen, want))
+        del graph
+    finally:
+        pa.pa_set_debug_checks(True)
+    assert pa.pa_check_device_errors() == 0
+
+
 def test_append_of_a_ragged_batch_reports_what_it_skips():
     rng = np.random.default_rng(12)
     new = np.array([1] * 40 + [600] + [2] * 20)
