@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) rope_store_any_kernel(const RopeStor
 template <int D>
 cudaError_t launch_d(const RopeStoreParams& p, cudaStream_t stream) {
   // Tokens a CTA takes: one while they leave SMs free (64 tokens: 2.3 us against 2.5 with two),
-  // two beyond four CTAs an SM (1147 tokens: 6.8 us against 8.5 with one and 7.9 with four),
+  // two beyond four CTAs an SM (1159 tokens: 6.8 us against 8.5 with one and 7.9 with four),
   // four for long chunks, whose set-up then weighs least (16384 tokens: 69.3 us against 69.9
   // with two and 92 with one).
   const int64_t sms = sm_count();

@@ -853,7 +853,7 @@ cudaError_t launch_append_blockscale(const AppendLaunch& a, cudaStream_t stream)
   p.err = device_error_word();
   // Few tokens: one launch, whose first CTAs turn the queries. Many: the queries' own kernel
   // (64 registers against the units' 128, so twice the warps stream them), beside whose last
-  // CTAs the units of many rows may start (16384 tokens 82.7 -> 80.0 us, 1147 16.6 -> 15.6).
+  // CTAs the units of many rows may start (16384 tokens 82.7 -> 80.0 us, 3010 16.6 -> 15.6).
   const bool q_here = a.num_tokens <= 8 * sm_count();
   p.behind_queries = !q_here && a.num_q_heads > 0;
   if (!q_here && a.num_q_heads > 0) {
