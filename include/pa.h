@@ -508,7 +508,8 @@ pa_status pa_rope_store_kvcache(void* q_out, int64_t q_out_stride, const void* q
  *   k, v            bf16 [num_tokens, Hkv, D], strides as in pa_rope.
  *   cu_seqlens_q    int32 [num_seqs + 1], device; context_lens int32 [num_seqs], including
  *                   the new tokens.
- *   max_q_len       host upper bound of the new tokens of one sequence.
+ *   max_q_len       host upper bound of the new tokens of one sequence (0: there are none,
+ *                   and no length is looked at).
  * No two sequences of a call may append to one block, and a block that other sequences read
  * is copied first (copy-on-write). Rows past the new ones stay as they are. A sequence whose
  * lengths do not fit (n_new above context_lens, max_q_len or num_tokens, a context past the
@@ -526,7 +527,8 @@ pa_status pa_store_kvcache_fp8_blockscale(const void* k, int64_t k_stride, const
 /*
  * pa_rope_store_kvcache_fp8_blockscale — q_out = pa_rope(q), then
  * pa_store_kvcache_fp8_blockscale(pa_rope(k), v), in one launch and with the same bits.
- * positions int32 [num_tokens]; q, q_out and num_q_heads as in pa_rope_store_kvcache.
+ * positions int32 [num_tokens]; q, q_out and num_q_heads as in pa_rope_store_kvcache (the
+ * queries of all num_tokens tokens are turned, of padding behind the last sequence too).
  * rot_dim must be a multiple of 16 (else PA_ERR_UNSUPPORTED: use the two calls).
  */
 pa_status pa_rope_store_kvcache_fp8_blockscale(

@@ -633,11 +633,12 @@ pa_status pa_rope_store_kvcache_fp8_blockscale(
   if (st != PA_OK) return st;
   if (num_seqs < 0 || num_tokens < 0 || max_q_len < 0 || num_q_heads < 0 || max_blocks_per_seq <= 0)
     return PA_ERR_INVALID_ARG;
-  if (num_tokens == 0 || (num_seqs == 0 && num_q_heads == 0)) return PA_OK;
+  const bool rows = num_seqs > 0 && max_q_len > 0;
+  if (num_tokens == 0 || (!rows && num_q_heads == 0)) return PA_OK;
   st = check_rope(rope, cache.head_dim, positions);
   if (st != PA_OK) return st;
   if (rope.rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
-  if (num_seqs == 0)  // nothing to append; the tokens' queries are turned all the same
+  if (!rows)  // nothing to append; the tokens' queries are turned all the same
     return pa_rope(q_out, q_out_stride, q, q_stride, num_tokens, num_q_heads, cache.head_dim, positions,
                    rope, stream);
   if (num_q_heads > 0 && (!rows_ok(q, q_stride, num_q_heads, cache.head_dim) ||
