@@ -32,8 +32,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kFewRows = 32;    // new rows of a block that one warp takes
 constexpr int kWindow = 1024;   // sequences whose units are counted at a time
-constexpr int kRowHeads = 8;    // (row, head) pairs a thread keeps in registers (64 registers)
-constexpr int kMaxCluster = 4;  // CTAs that share a block of 1024 rows
+constexpr int kMaxCluster = 8;  // CTAs that share a block of 1024 rows
 constexpr int kQTokens = 2;        // tokens of a CTA that turns queries
 
 struct AppendParams {
@@ -435,8 +434,9 @@ __device__ __forceinline__ void append_few(const AppendParams& p, const Span& u,
     requantise_rows<D>(codes, row_bytes, u.r0, __fdiv_rn(old, scale), lane, 32);
 }
 
-// Many new rows per block. A CTA takes RL * kRowHeads / HT rows of HT heads (64 rows of 4
-// heads, 128 of 2 or 256 of one at 128 dims), all in registers between the scan for the
+// Many new rows per block. A thread keeps RH (row, head) pairs in registers (8: 64 registers), so
+// a CTA takes RL * RH / HT rows of HT heads (RH 8: 64 rows of 4 heads, 128 of 2 or 256 of one
+// at 128 dims), all in registers between the scan for the
 // largest magnitude and the quantising; a block with more rows is shared by a cluster of CTAs,
 // which exchange their largest magnitudes through distributed shared memory. HT is the
 // largest that holds a block's rows in one CTA: the turns of a row are then formed once for
@@ -445,10 +445,10 @@ __device__ __forceinline__ void append_few(const AppendParams& p, const Span& u,
 // of one head, 16384 tokens of 8 kv heads: a cluster waits for its slowest load.)
 // Turns: two tables in shared memory, the high and the low factor (rope.cuh) of the CTA's
 // consecutive positions; a row whose position does not follow is turned by the series.
-template <int D, int HT>
+template <int D, int HT, int RH>
 struct ManyShared {
   static constexpr int RL = kThreads / (D / 16);  // rows side by side
-  static constexpr int RT = kRowHeads / HT;       // rows per thread
+  static constexpr int RT = RH / HT;              // rows per thread
   static constexpr int CAP = RL * RT;             // rows of a CTA
   static constexpr int HIGH = CAP / kRopeLow + 1;
   RopeTable<HIGH, D / 2> high;
@@ -457,10 +457,10 @@ struct ManyShared {
   unsigned cta_top[kMaxCluster][HT];
 };
 
-template <int D, int HT>
+template <int D, int HT, int RH>
 __device__ __forceinline__ void append_many(const AppendParams& p, const Span& u, bool is_v, int g,
-                                            ManyShared<D, HT>& tables) {
-  using M = ManyShared<D, HT>;
+                                            ManyShared<D, HT, RH>& tables) {
+  using M = ManyShared<D, HT, RH>;
   constexpr int NG = D / 16, RL = M::RL, RT = M::RT, CAP = M::CAP, HIGH = M::HIGH;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = p.cluster, rank = static_cast<int>(cluster.block_rank());
@@ -617,11 +617,11 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams
 
 // The same with a CTA or a cluster per unit of HT heads. (BEHIND at compile time: the wait in the
 // code took calls of a few tokens 0.15 us.)
-template <int D, int HT, bool BEHIND>
-__global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendParams p) {
+template <int D, int HT, int RH, bool BEHIND>
+__global__ void __launch_bounds__(kThreads, RH == 8 ? 2 : 3) append_many_kernel(const AppendParams p) {
   __shared__ union {
     RopeTable<kQTokens, D / 2> queries;
-    ManyShared<D, HT> many;
+    ManyShared<D, HT, RH> many;
   } sm;
   if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {  // whole clusters
     turn_queries<D>(p, sm.queries);
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const AppendPa
   rest /= hgroups;
   const Seq q = seq_of(p, s, threadIdx.x == 0);
   if ((rest >> 1) < blocks_of(p, q))
-    append_many<D, HT>(p, span_of(p, q, s, rest >> 1), rest & 1, g, sm.many);
+    append_many<D, HT, RH>(p, span_of(p, q, s, rest >> 1), rest & 1, g, sm.many);
   // complete, for what follows in the stream, only once the queries' kernel is
   if (BEHIND && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_ragged_kernel(const Append
   constexpr int FEW = MANY ? kFewRows / 2 : kFewRows;  // beside many rows' registers, half as many
   __shared__ union {
     RopeTable<kQTokens, D / 2> queries;
-    ManyShared<D, 1> many;
+    ManyShared<D, 1, 8> many;
   } sm;
   __shared__ long long first_unit[kWindow];
   __shared__ Seq seqs[kWindow];
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_ragged_kernel(const Append
           const int j = static_cast<int>(at / many_units), rest = static_cast<int>(at - j * static_cast<int64_t>(many_units));
           const bool is_v = rest >= p.num_kv_heads;
           __syncthreads();  // the tables are free
-          append_many<D, 1>(p, span_of(p, q, s0 + i, j + b.first), is_v,
+          append_many<D, 1, 8>(p, span_of(p, q, s0 + i, j + b.first), is_v,
                             is_v ? rest - p.num_kv_heads : rest, sm.many);
           continue;
         }
@@ -786,37 +786,63 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
     const int grid = p.num_q_heads > 0 && p.num_tokens > p.num_seqs ? p.num_tokens : p.num_seqs;
     return launch(append_one_kernel<D>, p, grid, stream);
   }
-  constexpr int CAP = ManyShared<D, 1>::CAP;  // rows of one head that a CTA holds
-  static_assert(kMaxCluster * CAP >= 1024, "the largest block");
-  const int ht = p.num_kv_heads % 4 == 0 && rows <= CAP / 4 ? 4 : p.num_kv_heads % 2 == 0 && rows <= CAP / 2 ? 2 : 1;
+  constexpr int CAP = ManyShared<D, 1, 8>::CAP;  // rows of one head that a CTA holds
   const bool few = rows <= kFewRows;
   if (few) p.behind_queries = false;
-  while (!few && p.cluster * CAP < rows * ht) p.cluster *= 2;
-  p.q_ctas = (p.q_ctas + p.cluster - 1) / p.cluster * p.cluster;
+  // heads and CTAs of a unit of many rows, when a thread keeps rh (row, head) pairs
+  int ht, cluster;
+  auto shape = [&](int rh) {
+    const int cap = CAP * rh / 8;
+    ht = p.num_kv_heads % 4 == 0 && rh == 8 && rows <= cap / 4 ? 4 : p.num_kv_heads % 2 == 0 && rows <= cap / 2 ? 2 : 1;
+    cluster = 1;
+    while (!few && cluster * cap < rows * ht) cluster *= 2;
+  };
+  static_assert(kMaxCluster * CAP / 2 >= 1024, "the largest block");
+  shape(8);
   const int64_t spans = static_cast<int64_t>(p.num_seqs) * p.span;
-  const int64_t ctas = few ? (spans * 2 * p.num_kv_heads + kThreads / 32 - 1) / (kThreads / 32)
-                           : spans * 2 * (p.num_kv_heads / ht) * p.cluster;
+  auto ctas_of = [&]() {
+    return few ? (spans * 2 * p.num_kv_heads + kThreads / 32 - 1) / (kThreads / 32)
+               : spans * 2 * (p.num_kv_heads / ht) * cluster;
+  };
+  int64_t ctas = ctas_of();
   // Counting pays beyond four waves of CTAs, when the blocks would hold an eighth of the most
   // rows on average. Without / with it, us (32 q and 8 kv heads): 255 single tokens and a chunk
   // of 8192, blocks of 256, 400 / 59; 63 and 2048 47 / 21; 15 and 2048 24.1 / 20.5; 63 and 512,
   // blocks of 16, 20.2 / 13.9; on the other side 63 and 40, blocks of 64 (1.7 waves) 7.5 / 8.5, 98
   // ragged of up to 45 (a quarter full) 15.2 / 20.5, 64 even chunks of 256 82 / 97.
   const int64_t sms = sm_count();
+  auto set_cluster = [&]() {
+    p.cluster = cluster;
+    p.q_ctas = (p.q_ctas + cluster - 1) / cluster * cluster;  // whole clusters
+  };
   if (ctas > 8 * sms && static_cast<int64_t>(p.num_tokens) * 8 < spans * rows) {
     // as many CTAs as are resident (not beside the queries' kernel: 63 and 2048 took 22.5 us)
     p.behind_queries = false;
+    set_cluster();
     const int64_t grid = p.q_ctas + 2 * sms / p.cluster * p.cluster;
     return few ? launch(append_ragged_kernel<D, false>, p, grid, stream)
                : launch(append_ragged_kernel<D, true>, p, grid, stream);
   }
   if (few) return launch(append_few_kernel<D>, p, p.q_ctas + ctas, stream);
+  // Half the pairs a thread (three CTAs an SM) when the units of eight leave SMs idle, or hold one
+  // head's rows twice over. With eight / four, us: 1024 tokens of 8 heads, blocks of 256, 10.1 / 8.8,
+  // of 64 8.9 / 8.1; 16384 of 3 heads, blocks of 64, 37.7 / 31.0; 4096 of 8, blocks of 256, 17.4 / 19.5.
+  const bool half = ctas <= sms || (ht == 1 && rows <= CAP / 2);
+  if (half) {
+    shape(4);
+    ctas = ctas_of();
+  }
+  set_cluster();
   auto many = [&](auto plain, auto behind) {
     return p.behind_queries ? launch(behind, p, p.q_ctas + ctas, stream)
                             : launch(plain, p, p.q_ctas + ctas, stream);
   };
-  if (ht == 4) return many(append_many_kernel<D, 4, false>, append_many_kernel<D, 4, true>);
-  if (ht == 2) return many(append_many_kernel<D, 2, false>, append_many_kernel<D, 2, true>);
-  return many(append_many_kernel<D, 1, false>, append_many_kernel<D, 1, true>);
+  if (half)
+    return ht == 2 ? many(append_many_kernel<D, 2, 4, false>, append_many_kernel<D, 2, 4, true>)
+                   : many(append_many_kernel<D, 1, 4, false>, append_many_kernel<D, 1, 4, true>);
+  if (ht == 4) return many(append_many_kernel<D, 4, 8, false>, append_many_kernel<D, 4, 8, true>);
+  if (ht == 2) return many(append_many_kernel<D, 2, 8, false>, append_many_kernel<D, 2, 8, true>);
+  return many(append_many_kernel<D, 1, 8, false>, append_many_kernel<D, 1, 8, true>);
 }
 
 }  // namespace

@@ -82,6 +82,12 @@ def same_codes(got, want):
     (2, 64, 128, [2500, 77], [100, 127]),
     (3, 128, 256, [3000], [1]),
     (2, 128, 1024, [1500, 900], [700, 0]),                    # blocks read twice
+    # many units: eight (row, head) pairs a thread, of 2, 4 and 1 heads, a block by one CTA and by several
+    (2, 128, 128, [6000, 3000], [5, 127]),
+    (4, 64, 128, [5000, 4000, 3000], [1, 64, 120]),
+    (2, 64, 256, [6000, 5000, 4000], [0, 9, 255]),
+    (8, 128, 1024, [1500, 900, 2000], [1000, 3, 512]),
+    (3, 64, 512, [2000, 3000, 1000, 2500, 1500, 700], [1, 2, 3, 4, 500, 511]),
     # one long chunk beside many short ones
     (8, 128, 16, [1] * 30 + [700] + [2, 0, 17, 5] * 8, list(range(63))),
     (8, 128, 64, [1] * 20 + [33, 17, 16, 0] + [600] + [1] * 20, list(range(40, 85))),
