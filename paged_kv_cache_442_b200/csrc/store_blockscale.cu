@@ -30,7 +30,8 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFewRows = 32;    // new rows of a block that one warp takes
+constexpr int kFewRows = 16;    // most new rows of a block that one warp takes ...
+constexpr int kVeryFewRows = 8;  // ... and of a kernel that keeps half the registers for them
 constexpr int kWindow = 1024;   // sequences whose units are counted at a time
 constexpr int kMaxCluster = 8;  // CTAs that share a block of 1024 rows
 constexpr int kQTokens = 2;        // tokens of a CTA that turns queries
@@ -594,7 +595,7 @@ __device__ __forceinline__ void append_many(const AppendParams& p, const Span& u
 
 // The units as the host bounds them: max_new rows' blocks for every sequence, of which those
 // past a sequence's own have nothing to do. Few rows a block: a warp per unit.
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams p) {
   __shared__ RopeTable<kQTokens, D / 2> table;
   if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const AppendParams
   rest /= p.num_kv_heads;
   const Seq q = seq_of(p, s, lane == 0);
   if ((rest >> 1) < blocks_of(p, q))
-    append_few<D, kFewRows>(p, span_of(p, q, s, rest >> 1), rest & 1, g, lane);
+    append_few<D, ROWS>(p, span_of(p, q, s, rest >> 1), rest & 1, g, lane);
 }
 
 // The same with a CTA or a cluster per unit of HT heads. (BEHIND at compile time: the wait in the
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, RH == 8 ? 2 : 3) append_many_kernel(
 template <int D, bool MANY>
 __global__ void __launch_bounds__(kThreads, 2) append_ragged_kernel(const AppendParams p) {
   constexpr int kEach = kWindow / kThreads;
-  constexpr int FEW = MANY ? kFewRows / 2 : kFewRows;  // beside many rows' registers, half as many
+  constexpr int FEW = MANY ? kVeryFewRows : kFewRows;
   __shared__ union {
     RopeTable<kQTokens, D / 2> queries;
     ManyShared<D, 1, 8> many;
@@ -787,30 +788,34 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
     return launch(append_one_kernel<D>, p, grid, stream);
   }
   constexpr int CAP = ManyShared<D, 1, 8>::CAP;  // rows of one head that a CTA holds
-  const bool few = rows <= kFewRows;
-  if (few) p.behind_queries = false;
   // heads and CTAs of a unit of many rows, when a thread keeps rh (row, head) pairs
   int ht, cluster;
+  int64_t ctas;
+  const int64_t spans = static_cast<int64_t>(p.num_seqs) * p.span;
   auto shape = [&](int rh) {
     const int cap = CAP * rh / 8;
     ht = p.num_kv_heads % 4 == 0 && rh == 8 && rows <= cap / 4 ? 4 : p.num_kv_heads % 2 == 0 && rows <= cap / 2 ? 2 : 1;
     cluster = 1;
-    while (!few && cluster * cap < rows * ht) cluster *= 2;
+    while (cluster * cap < rows * ht) cluster *= 2;
+    ctas = spans * 2 * (p.num_kv_heads / ht) * cluster;
   };
   static_assert(kMaxCluster * CAP / 2 >= 1024, "the largest block");
   shape(8);
-  const int64_t spans = static_cast<int64_t>(p.num_seqs) * p.span;
-  auto ctas_of = [&]() {
-    return few ? (spans * 2 * p.num_kv_heads + kThreads / 32 - 1) / (kThreads / 32)
-               : spans * 2 * (p.num_kv_heads / ht) * cluster;
-  };
-  int64_t ctas = ctas_of();
+  const int64_t sms = sm_count();
+  // A warp forms its rows' turns for one head, a CTA for all of its heads, but a CTA waits for its
+  // rows together: warps up to 8 rows, or up to 16 when the CTAs would fill four waves. Warps /
+  // CTAs, us: 64 sequences of 16 rows 11.6 / 9.0, 256 of 12 20.2 / 24.3, 512 tokens in blocks of 16
+  // 10.3 / 6.5, 16000 61.5 / 74.0; 64 of 30 21.0 (with registers for 32 rows) / 11.5.
+  const bool few = rows <= kVeryFewRows || (rows <= kFewRows && ctas > 8 * sms);
+  if (few) {
+    p.behind_queries = false;
+    ctas = (spans * 2 * p.num_kv_heads + kThreads / 32 - 1) / (kThreads / 32);
+  }
   // Counting pays beyond four waves of CTAs, when the blocks would hold an eighth of the most
   // rows on average. Without / with it, us (32 q and 8 kv heads): 255 single tokens and a chunk
-  // of 8192, blocks of 256, 400 / 59; 63 and 2048 47 / 21; 15 and 2048 24.1 / 20.5; 63 and 512,
-  // blocks of 16, 20.2 / 13.9; on the other side 63 and 40, blocks of 64 (1.7 waves) 7.5 / 8.5, 98
+  // of 8192, blocks of 256, 400 / 58; 63 and 2048 47 / 21; 15 and 2048 24.1 / 20.5; 63 and 512,
+  // blocks of 16, 20.2 / 12.4; on the other side 63 and 40, blocks of 64 (1.7 waves) 7.5 / 8.5, 98
   // ragged of up to 45 (a quarter full) 15.2 / 20.5, 64 even chunks of 256 82 / 97.
-  const int64_t sms = sm_count();
   auto set_cluster = [&]() {
     p.cluster = cluster;
     p.q_ctas = (p.q_ctas + cluster - 1) / cluster * cluster;  // whole clusters
@@ -823,15 +828,14 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
     return few ? launch(append_ragged_kernel<D, false>, p, grid, stream)
                : launch(append_ragged_kernel<D, true>, p, grid, stream);
   }
-  if (few) return launch(append_few_kernel<D>, p, p.q_ctas + ctas, stream);
+  if (few)
+    return rows <= kVeryFewRows ? launch(append_few_kernel<D, kVeryFewRows>, p, p.q_ctas + ctas, stream)
+                                : launch(append_few_kernel<D, kFewRows>, p, p.q_ctas + ctas, stream);
   // Half the pairs a thread (three CTAs an SM) when the units of eight leave SMs idle, or hold one
   // head's rows twice over. With eight / four, us: 1024 tokens of 8 heads, blocks of 256, 10.1 / 8.8,
   // of 64 8.9 / 8.1; 16384 of 3 heads, blocks of 64, 37.7 / 31.0; 4096 of 8, blocks of 256, 17.4 / 19.5.
   const bool half = ctas <= sms || (ht == 1 && rows <= CAP / 2);
-  if (half) {
-    shape(4);
-    ctas = ctas_of();
-  }
+  if (half) shape(4);
   set_cluster();
   auto many = [&](auto plain, auto behind) {
     return p.behind_queries ? launch(behind, p, p.q_ctas + ctas, stream)

@@ -87,6 +87,9 @@ def same_codes(got, want):
     (4, 64, 128, [5000, 4000, 3000], [1, 64, 120]),
     (2, 64, 256, [6000, 5000, 4000], [0, 9, 255]),
     (8, 128, 1024, [1500, 900, 2000], [1000, 3, 512]),
+    (8, 128, 16, [5000, 3000], [3, 16]),                      # sixteen rows a warp
+    (4, 64, 16, [9000, 7000], [15, 1]),
+    (8, 128, 64, [16, 9, 12, 1], [60, 0, 52, 3]),             # nine to sixteen rows a CTA
     (3, 64, 512, [2000, 3000, 1000, 2500, 1500, 700], [1, 2, 3, 4, 500, 511]),
     # one long chunk beside many short ones
     (8, 128, 16, [1] * 30 + [700] + [2, 0, 17, 5] * 8, list(range(63))),
