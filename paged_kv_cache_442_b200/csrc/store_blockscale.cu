@@ -435,6 +435,166 @@ __device__ __forceinline__ void append_few(const AppendParams& p, const Span& u,
     requantise_rows<D>(codes, row_bytes, u.r0, __fdiv_rn(old, scale), lane, 32);
 }
 
+// Both factors (rope.cuh) of the turns at ROWS consecutive positions; a position that does not
+// follow is turned by the series.
+template <int D, int ROWS>
+struct TurnTables {
+  static constexpr int HIGH = ROWS / kRopeLow + 1;
+  RopeTable<HIGH, D / 2> high;
+  RopeTable<kRopeLow, D / 2> low;
+
+  // base: the first position, its low bits cleared
+  __device__ __forceinline__ void fill(const RopeParams& r, unsigned base) {
+    // one frequency per thread, rows `apart` apart
+    const int half = r.rot_dim >> 1, tid = threadIdx.x;
+    const int apart = kThreads / half, row0 = tid / half, f = tid - row0 * half;
+    if (row0 < apart) {
+      const unsigned long long rate = rope_rate(__ldg(r.inv_freq + f));
+      for (int row = row0; row < kRopeLow; row += apart) low.put(row, f, rope_low(row, rate));
+      for (int row = row0; row < HIGH; row += apart)
+        high.put(row, f, rope_high(static_cast<int>(base + row * kRopeLow), rate, r.amplitude));
+    }
+  }
+  __device__ __forceinline__ RopeTurns at(const RopeParams& r, unsigned base, int pos, int grp) const {
+    const unsigned row = (static_cast<unsigned>(pos) - base) / kRopeLow;
+    RopeTurns cs;
+    if (row < HIGH) {
+      cs = rope_product(high.group(row, grp), low.group(pos & (kRopeLow - 1), grp));
+    } else {
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        const float2 t = rope_turn(pos, rope_rate(__ldg(r.inv_freq + 8 * grp + e)), r.amplitude);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k == e) set_turn(cs, k, t);
+      }
+    }
+    return cs;
+  }
+};
+
+// Chunks in blocks of 16 or 32: a CTA takes the new rows of 64 aligned positions (two or four
+// blocks) of HT heads, as below, with a largest magnitude for every block: a row's threads
+// agree by shuffles, the rows of a block by a maximum in shared memory.
+template <int D, int HT>
+struct TileShared {
+  static constexpr int kRows = 64;
+  static constexpr int kBlocks = 4;  // of 16 rows
+  TurnTables<D, kRows> turns;
+  unsigned top[kBlocks][HT];
+};
+
+template <int D, int HT>
+__device__ __forceinline__ void append_tile(const AppendParams& p, const Seq& q, int s, int j, bool is_v,
+                                            int g, TileShared<D, HT>& sm) {
+  constexpr int NG = D / 16, RL = kThreads / NG, RT = TileShared<D, HT>::kRows / RL;
+  constexpr int TILE = TileShared<D, HT>::kRows, NB = TileShared<D, HT>::kBlocks;
+  const int tid = threadIdx.x, grp = tid % NG, rl = tid / NG;
+  const int2 at = rope_vectors(grp, p.rope);
+  const int pos0 = q.ctx - q.n;
+  const int64_t start = static_cast<int64_t>(pos0 / TILE + j) * TILE;
+  const int lo = start > pos0 ? static_cast<int>(start) : pos0;
+  const int rows = static_cast<int>(min(start + TILE, static_cast<int64_t>(q.ctx)) - lo);
+  const int off = lo - static_cast<int>(start);  // of the first row
+  const int64_t tok0 = q.begin + (lo - pos0);
+  const int bs_mask = (1 << p.bs_log2) - 1;
+  const int32_t* ids = p.block_tables + static_cast<int64_t>(s) * p.max_blocks + (start >> p.bs_log2);
+  auto id_of = [&](int sub) { return __ldg(ids + sub); };
+  auto good = [&](int id) { return id >= 0 && id < p.num_blocks; };
+  const int64_t vstride = (is_v ? p.v_stride : p.k_stride) / 8;
+  const uint4* src = reinterpret_cast<const uint4*>(is_v ? p.v : p.k) + (tok0 + rl) * vstride + g * (D / 8);
+  uint4 a[RT][HT], b[RT][HT];
+  int id[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const uint4* row = src + i * (RL * vstride);
+    const int r = rl + i * RL;
+    id[i] = r < rows ? id_of((off + r) >> p.bs_log2) : 0;
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+      a[i][h] = b[i][h] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        a[i][h] = __ldg(row + h * (D / 8) + at.x);
+        b[i][h] = __ldg(row + h * (D / 8) + at.y);
+      }
+    }
+  }
+  // the first block may hold rows already
+  const int sub0 = off >> p.bs_log2, r0 = off & bs_mask;
+  const int id0 = id_of(sub0);
+  float* scales = (is_v ? p.v_scales : p.k_scales) + g;
+  float old[HT];
+#pragma unroll
+  for (int h = 0; h < HT; ++h)
+    old[h] = r0 && good(id0) ? __ldcg(scales + static_cast<int64_t>(id0) * p.num_kv_heads + h) : 0.f;
+  if (tid < NB * HT) sm.top[tid / HT][tid % HT] = 0;
+  const bool turns = !is_v && p.rope.rot_dim > 0;
+  const int32_t* pos = p.positions + tok0;
+  unsigned base = 0;
+  if (turns) {
+    base = static_cast<unsigned>(__ldg(pos)) & ~(kRopeLow - 1u);
+    sm.turns.fill(p.rope, base);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int r = rl + i * RL;
+    if (turns && r < rows && grp < (p.rope.rot_dim >> 4)) {
+      const RopeTurns cs = sm.turns.at(p.rope, base, __ldg(pos + r), grp);
+#pragma unroll
+      for (int h = 0; h < HT; ++h) rope_group(a[i][h], b[i][h], cs, p.rope.interleaved != 0);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+      const uint4 va[1] = {a[i][h]}, vb[1] = {b[i][h]};
+      unsigned t = top_of(va, vb);
+#pragma unroll
+      for (int o = NG / 2; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+      if (grp == 0 && r < rows) atomicMax(&sm.top[(off + r) >> p.bs_log2][h], t);
+    }
+  }
+  __syncthreads();
+  auto scale_of = [&](int sub, int h, float before) {
+    const float need = exp2_int(scale_exponent(sm.top[sub][h]));
+    return sub == sub0 && before >= need ? before : need;
+  };
+  uint8_t* pool = is_v ? p.v_codes : p.k_codes;
+  const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * D;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int r = rl + i * RL;
+    if (r >= rows) continue;
+    if (!good(id[i])) {
+      if (grp == 0) flag_error(p.err, PA_DEV_ERR_BAD_INDEX);
+      continue;
+    }
+    uint8_t* dst = pool + ((static_cast<int64_t>(id[i]) << p.bs_log2) + ((off + r) & bs_mask)) * row_bytes + g * D;
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+      const float inv = __frcp_rn(scale_of((off + r) >> p.bs_log2, h, old[h]));
+      *reinterpret_cast<uint2*>(dst + h * D + at.x * 8) = quantise8(a[i][h], inv);
+      *reinterpret_cast<uint2*>(dst + h * D + at.y * 8) = quantise8(b[i][h], inv);
+    }
+  }
+  if (r0 > 0 && good(id0)) {  // rows that were in the first block before, when its scale grew
+#pragma unroll
+    for (int h = 0; h < HT; ++h) {
+      const float scale = scale_of(sub0, h, old[h]);
+      if (scale != old[h])
+        requantise_rows<D>(pool + (static_cast<int64_t>(id0) << p.bs_log2) * row_bytes + (g + h) * D, row_bytes, r0,
+                           __fdiv_rn(old[h], scale), tid, kThreads);
+    }
+  }
+  const int sub = sub0 + tid / HT, h = tid % HT;
+  if (sub <= (off + rows - 1) >> p.bs_log2 && good(id_of(sub))) {  // a thread per block and head
+    float* to = scales + static_cast<int64_t>(id_of(sub)) * p.num_kv_heads + h;
+    const float before = sub == sub0 && r0 ? __ldcg(to) : 0.f;
+    const float scale = scale_of(sub, h, before);
+    if (scale != before) *to = scale;
+  }
+}
+
 // Many new rows per block. A thread keeps RH (row, head) pairs in registers (8: 64 registers), so
 // a CTA takes RL * RH / HT rows of HT heads (RH 8: 64 rows of 4 heads, 128 of 2 or 256 of one
 // at 128 dims), all in registers between the scan for the
@@ -451,9 +611,7 @@ struct ManyShared {
   static constexpr int RL = kThreads / (D / 16);  // rows side by side
   static constexpr int RT = RH / HT;              // rows per thread
   static constexpr int CAP = RL * RT;             // rows of a CTA
-  static constexpr int HIGH = CAP / kRopeLow + 1;
-  RopeTable<HIGH, D / 2> high;
-  RopeTable<kRopeLow, D / 2> low;
+  TurnTables<D, CAP> turns;
   unsigned warp_top[kThreads / 32][HT];
   unsigned cta_top[kMaxCluster][HT];
 };
@@ -462,7 +620,7 @@ template <int D, int HT, int RH>
 __device__ __forceinline__ void append_many(const AppendParams& p, const Span& u, bool is_v, int g,
                                             ManyShared<D, HT, RH>& tables) {
   using M = ManyShared<D, HT, RH>;
-  constexpr int NG = D / 16, RL = M::RL, RT = M::RT, CAP = M::CAP, HIGH = M::HIGH;
+  constexpr int NG = D / 16, RL = M::RL, RT = M::RT, CAP = M::CAP;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = p.cluster, rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x;
@@ -503,35 +661,13 @@ __device__ __forceinline__ void append_many(const AppendParams& p, const Span& u
     // both factors of the CTA's positions, while its rows are on their way
     const int32_t* pos = p.positions + u.tok0;
     const unsigned base = static_cast<unsigned>(__ldg(pos + rank * CAP)) & ~(kRopeLow - 1u);
-    // one frequency per thread, rows `apart` apart
-    const int apart = kThreads / half, row0 = tid / half, f = tid - row0 * half;
-    if (row0 < apart) {
-      const unsigned long long rate = rope_rate(__ldg(p.rope.inv_freq + f));
-      for (int row = row0; row < kRopeLow; row += apart) tables.low.put(row, f, rope_low(row, rate));
-      for (int row = row0; row < HIGH; row += apart)
-        tables.high.put(row, f, rope_high(static_cast<int>(base + row * kRopeLow), rate, p.rope.amplitude));
-    }
+    tables.turns.fill(p.rope, base);
     __syncthreads();
     if (turned) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         if (mine + i * RL >= u.rows) continue;
-        const int at_pos = __ldg(pos + mine + i * RL);
-        const unsigned high = (static_cast<unsigned>(at_pos) - base) / kRopeLow;
-        RopeTurns cs;
-        if (high < HIGH) {
-          cs = rope_product(tables.high.group(high, grp),
-                            tables.low.group(at_pos & (kRopeLow - 1), grp));
-        } else {
-#pragma unroll 1
-          for (int e = 0; e < 8; ++e) {
-            const float2 t = rope_turn(at_pos, rope_rate(__ldg(p.rope.inv_freq + 8 * grp + e)),
-                                       p.rope.amplitude);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k == e) set_turn(cs, k, t);
-          }
-        }
+        const RopeTurns cs = tables.turns.at(p.rope, base, __ldg(pos + mine + i * RL), grp);
 #pragma unroll
         for (int h = 0; h < HT; ++h) rope_group(a[i][h], b[i][h], cs, p.rope.interleaved != 0);
       }
@@ -638,6 +774,32 @@ __global__ void __launch_bounds__(kThreads, RH == 8 ? 2 : 3) append_many_kernel(
   const Seq q = seq_of(p, s, threadIdx.x == 0);
   if ((rest >> 1) < blocks_of(p, q))
     append_many<D, HT, RH>(p, span_of(p, q, s, rest >> 1), rest & 1, g, sm.many);
+  // complete, for what follows in the stream, only once the queries' kernel is
+  if (BEHIND && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A CTA per 64 positions and HT heads.
+template <int D, int HT, bool BEHIND>
+__global__ void __launch_bounds__(kThreads, HT == 4 ? 2 : 3) append_tile_kernel(const AppendParams p) {
+  __shared__ union {
+    RopeTable<kQTokens, D / 2> queries;
+    TileShared<D, HT> tile;
+  } sm;
+  if (blockIdx.x < static_cast<unsigned>(p.q_ctas)) {
+    turn_queries<D>(p, sm.queries);
+    return;
+  }
+  const int64_t unit = blockIdx.x - p.q_ctas;
+  const int hgroups = p.num_kv_heads / HT;
+  const int64_t per_seq = static_cast<int64_t>(p.span) * 2 * hgroups;
+  const int s = static_cast<int>(unit / per_seq);
+  int rest = static_cast<int>(unit - s * per_seq);
+  const int g = rest % hgroups * HT;
+  rest /= hgroups;
+  const Seq q = seq_of(p, s, threadIdx.x == 0);
+  constexpr int TILE = TileShared<D, HT>::kRows;
+  if (q.n > 0 && (rest >> 1) <= (q.ctx - 1) / TILE - (q.ctx - q.n) / TILE)
+    append_tile<D, HT>(p, q, s, rest >> 1, rest & 1, g, sm.tile);
   // complete, for what follows in the stream, only once the queries' kernel is
   if (BEHIND && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -804,9 +966,10 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
   const int64_t sms = sm_count();
   // A warp forms its rows' turns for one head, a CTA for all of its heads, but a CTA waits for its
   // rows together: warps up to 8 rows, or up to 16 when the CTAs would fill four waves. Warps /
-  // CTAs, us: 64 sequences of 16 rows 11.6 / 9.0, 256 of 12 20.2 / 24.3, 512 tokens in blocks of 16
-  // 10.3 / 6.5, 16000 61.5 / 74.0; 64 of 30 21.0 (with registers for 32 rows) / 11.5.
+  // CTAs, us: 64 sequences of 16 rows 11.6 / 9.0, 256 of 12 20.2 / 24.3; 64 of 30 21.0 (with registers
+  // for 32 rows) / 11.5.
   const bool few = rows <= kVeryFewRows || (rows <= kFewRows && ctas > 8 * sms);
+  const bool behind = p.behind_queries;
   if (few) {
     p.behind_queries = false;
     ctas = (spans * 2 * p.num_kv_heads + kThreads / 32 - 1) / (kThreads / 32);
@@ -814,7 +977,7 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
   // Counting pays beyond four waves of CTAs, when the blocks would hold an eighth of the most
   // rows on average. Without / with it, us (32 q and 8 kv heads): 255 single tokens and a chunk
   // of 8192, blocks of 256, 400 / 58; 63 and 2048 47 / 21; 15 and 2048 24.1 / 20.5; 63 and 512,
-  // blocks of 16, 20.2 / 12.4; on the other side 63 and 40, blocks of 64 (1.7 waves) 7.5 / 8.5, 98
+  // blocks of 16, 15.7 / 12.4; on the other side 63 and 40, blocks of 64 (1.7 waves) 7.5 / 8.5, 98
   // ragged of up to 45 (a quarter full) 15.2 / 20.5, 64 even chunks of 256 82 / 97.
   auto set_cluster = [&]() {
     p.cluster = cluster;
@@ -827,6 +990,23 @@ cudaError_t launch_d(AppendParams p, bool q_here, cudaStream_t stream) {
     const int64_t grid = p.q_ctas + 2 * sms / p.cluster * p.cluster;
     return few ? launch(append_ragged_kernel<D, false>, p, grid, stream)
                : launch(append_ragged_kernel<D, true>, p, grid, stream);
+  }
+  // Several small blocks a CTA. A unit a block / tiles, us: 8 sequences of 2000 rows and 8 heads in
+  // blocks of 16 61.7 / 48.5, of 32 52.9 / 48.4, of 500 in blocks of 16 24.5 / 17.3, 100 rows 4.1 / 4.5.
+  constexpr int TILE = TileShared<D, 1>::kRows;
+  if (bs < TILE && p.max_new > kFewRows) {
+    p.behind_queries = behind;
+    p.span = static_cast<int>((static_cast<int64_t>(p.max_new) + TILE - 2) / TILE) + 1;
+    const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.span * 2 * p.num_kv_heads;
+    // the most heads that leave no SM idle
+    ht = p.num_kv_heads % 4 == 0 && heads > 4 * sms ? 4 : p.num_kv_heads % 2 == 0 && heads > 2 * sms ? 2 : 1;
+    const int64_t grid = p.q_ctas + heads / ht;
+    auto tiles = [&](auto plain, auto beside) {
+      return behind ? launch(beside, p, grid, stream) : launch(plain, p, grid, stream);
+    };
+    if (ht == 4) return tiles(append_tile_kernel<D, 4, false>, append_tile_kernel<D, 4, true>);
+    if (ht == 2) return tiles(append_tile_kernel<D, 2, false>, append_tile_kernel<D, 2, true>);
+    return tiles(append_tile_kernel<D, 1, false>, append_tile_kernel<D, 1, true>);
   }
   if (few)
     return rows <= kVeryFewRows ? launch(append_few_kernel<D, kVeryFewRows>, p, p.q_ctas + ctas, stream)

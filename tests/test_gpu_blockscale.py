@@ -87,8 +87,14 @@ def same_codes(got, want):
     (4, 64, 128, [5000, 4000, 3000], [1, 64, 120]),
     (2, 64, 256, [6000, 5000, 4000], [0, 9, 255]),
     (8, 128, 1024, [1500, 900, 2000], [1000, 3, 512]),
-    (8, 128, 16, [5000, 3000], [3, 16]),                      # sixteen rows a warp
+    (8, 128, 64, [12] * 300, list(range(300))),               # up to sixteen rows a warp
+    (4, 64, 16, [16, 9, 0, 3] * 200, list(range(800))),
+    (8, 128, 16, [5000, 3000], [3, 16]),                      # several blocks a CTA, of 4, 2 and 1 heads
     (4, 64, 16, [9000, 7000], [15, 1]),
+    (2, 128, 32, [6000, 33], [5, 31]),
+    (2, 64, 32, [5000], [40]),
+    (3, 128, 16, [17, 100, 0, 63, 1], [15, 47, 9, 1, 63]),
+    (1, 128, 32, [500, 64], [95, 64]),
     (8, 128, 64, [16, 9, 12, 1], [60, 0, 52, 3]),             # nine to sixteen rows a CTA
     (3, 64, 512, [2000, 3000, 1000, 2500, 1500, 700], [1, 2, 3, 4, 500, 511]),
     # one long chunk beside many short ones
@@ -122,7 +128,8 @@ def test_append_matches_the_oracle_bit_for_bit(hkv, d, bs, new, old):
                                            ([70, 3], 64, True), ([300, 129, 1000], 256, True), ([5, 20], 32, True),
                                            ([1024 + 700], 1024, True), ([400], 512, False),
                                            ([1] * 150 + [900] + [20, 1, 2] * 9, 256, True),
-                                           ([3] * 200 + [600], 16, True)])
+                                           ([3] * 200 + [600], 16, True), ([300, 77, 1], 16, True),
+                                           ([200, 55], 32, False)])
 def test_rope_append_equals_rope_then_append(new, bs, steady, inter, rot):
     """steady: positions follow one another, as a rule; else they are anywhere."""
     rng = np.random.default_rng(rot + bs)
@@ -241,6 +248,29 @@ def test_a_long_append_is_complete_for_what_follows(bs):
     finally:
         pa.pa_set_debug_checks(True)
     assert pa.pa_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("bs", [16, 32])
+def test_append_of_small_blocks_skips_a_bad_one(bs):
+    rng = np.random.default_rng(13)
+    hkv, d, new, old = 2, 128, np.array([100, 70]), 9
+    ctx = new + old
+    tables, nb = tables_of(rng, ctx, bs)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    k = wild_rows(rng, int(cu[-1]), hkv, d)
+    kc, ks = pools_of(rng, nb, bs, hkv, d)
+    codes, scales = fp8_block.append(kc, ks, k, tables, cu, ctx)
+    for at, bad in (((0, 2), nb), ((1, 0), -1)):
+        t = [u8_dev(kc), u8_dev(kc), f32_dev(ks), f32_dev(ks)]
+        broken = tables.copy()
+        broken[at] = bad
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_store_kvcache_fp8_blockscale(bf16_dev(k), bf16_dev(k), *t, i32_dev(broken), i32_dev(cu), i32_dev(ctx), 100)
+        assert e.value.status == 3
+        want_c, want_s, left = codes.copy(), scales.copy(), int(tables[at])
+        want_c[left], want_s[left] = kc[left], ks[left]
+        for got_c, got_s in ((t[0], t[2]), (t[1], t[3])):
+            assert same_codes(got_c.cpu().numpy(), want_c) and np.array_equal(got_s.cpu().numpy(), want_s)
 
 
 def test_append_of_a_ragged_batch_reports_what_it_skips():
