@@ -8,12 +8,12 @@
 // scale grow, the stored codes move by an exact power of two: only codes that fall into
 // e4m3's subnormal range are rounded again.
 //
-// Work: one unit per (sequence, block its new rows reach, K or V, kv head or heads), 16 dims
-// per thread and row (two 16-byte loads). A unit loads its new rows into registers, turns them
-// (K), takes the largest finite magnitude on the bf16 bits, agrees on the scale and writes the
-// codes; rows already in the block are rewritten only when the scale grew. No unit shares a
-// (block, head) with another, so there are no global atomics and the result does not depend on
-// the order. HBM-bound: a bf16 row in, half of it out.
+// Work: one unit per (sequence, block its new rows reach, or 64 positions of small blocks, K or
+// V, kv head or heads), 16 dims per thread and row (two 16-byte loads). A unit loads its new
+// rows into registers, turns them (K), takes the largest finite magnitude on the bf16 bits,
+// agrees on the scale and writes the codes; rows already in the block are rewritten only when
+// the scale grew. No unit shares a (block, head) with another, so there are no global atomics
+// and the result does not depend on the order. HBM-bound: a bf16 row in, half of it out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -30,11 +30,11 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFewRows = 16;    // most new rows of a block that one warp takes ...
+constexpr int kFewRows = 16;     // most new rows of a block that one warp takes ...
 constexpr int kVeryFewRows = 8;  // ... and of a kernel that keeps half the registers for them
-constexpr int kWindow = 1024;   // sequences whose units are counted at a time
-constexpr int kMaxCluster = 8;  // CTAs that share a block of 1024 rows
-constexpr int kQTokens = 2;        // tokens of a CTA that turns queries
+constexpr int kWindow = 1024;    // sequences whose units are counted at a time
+constexpr int kMaxCluster = 8;   // CTAs that share a block of 1024 rows
+constexpr int kQTokens = 2;      // tokens of a CTA that turns queries
 
 struct AppendParams {
   const __nv_bfloat16* q;
@@ -595,17 +595,16 @@ __device__ __forceinline__ void append_tile(const AppendParams& p, const Seq& q,
   }
 }
 
-// Many new rows per block. A thread keeps RH (row, head) pairs in registers (8: 64 registers), so
-// a CTA takes RL * RH / HT rows of HT heads (RH 8: 64 rows of 4 heads, 128 of 2 or 256 of one
-// at 128 dims), all in registers between the scan for the
-// largest magnitude and the quantising; a block with more rows is shared by a cluster of CTAs,
-// which exchange their largest magnitudes through distributed shared memory. HT is the
-// largest that holds a block's rows in one CTA: the turns of a row are then formed once for
-// HT heads, and a row's HT heads (256 bytes each) are read together. (Clusters of 64 rows of
-// 4 heads for blocks of 256 measured 37.5 us without turns against 25 for one CTA of 256 rows
-// of one head, 16384 tokens of 8 kv heads: a cluster waits for its slowest load.)
-// Turns: two tables in shared memory, the high and the low factor (rope.cuh) of the CTA's
-// consecutive positions; a row whose position does not follow is turned by the series.
+// Many new rows per block. A thread keeps RH (row, head) pairs in registers (8: 64 registers),
+// so a CTA takes RL * RH / HT rows of HT heads (RH 8: 64 rows of 4 heads, 128 of 2 or 256 of
+// one at 128 dims), all in registers between the scan for the largest magnitude and the
+// quantising; a block with more rows is shared by a cluster of CTAs, which exchange their
+// largest magnitudes through distributed shared memory. HT is the largest that holds a block's
+// rows in one CTA: the turns of a row are then formed once for HT heads, and a row's HT heads
+// (256 bytes each) are read together. (Clusters of 64 rows of 4 heads for blocks of 256
+// measured 37.5 us without turns against 25 for one CTA of 256 rows of one head, 16384 tokens
+// of 8 kv heads: a cluster waits for its slowest load. With the turns that case's launch takes
+// 40 us, 2.5 TB/s: bound by each CTA's loads and stores not overlapping.)
 template <int D, int HT, int RH>
 struct ManyShared {
   static constexpr int RL = kThreads / (D / 16);  // rows side by side
