@@ -180,18 +180,23 @@ __global__ void __launch_bounds__(kThreads) rope_store_any_kernel(const RopeStor
 
 template <int D>
 cudaError_t launch_d(const RopeStoreParams& p, cudaStream_t stream) {
-  // Tokens a CTA takes: one while they leave SMs free (64 tokens: 2.3 us against 2.5 with two),
-  // two beyond four CTAs an SM (1159 tokens: 6.8 us against 8.5 with one and 7.9 with four),
-  // four for long chunks, whose set-up then weighs least (16384 tokens: 69.3 us against 69.9
-  // with two and 92 with one).
+  // Tokens a CTA takes: one while they leave SMs free (64 tokens: 2.3 us against 2.5 with two).
+  // Beyond four CTAs an SM two of many heads (1159 tokens of 32 q and 8 kv heads 6.8 us against 8.5
+  // with one and 7.9 with four), four of fewer, whose heads do not fill a CTA (4000 tokens of 4 and 2
+  // heads 5.7 against 7.9 with two) and eight when they are fewest (4.7 against 5.7 with four; 24 heads
+  // 12.1 against 11.5). Four for long chunks, whose set-up then weighs least (16384 tokens: 69.3 us
+  // against 69.9 with two and 92 with one).
   const int64_t sms = sm_count();
   auto launch = [&](auto kernel, int tb) {
     kernel<<<static_cast<unsigned>((p.num_tokens + tb - 1) / tb), kThreads, 0, stream>>>(p);
   };
+  const int64_t wide = (p.num_q_heads + 2 * static_cast<int64_t>(p.num_kv_heads)) * D;  // values of a token
   if (p.num_tokens <= 4 * sms) {
     launch(rope_store_kernel<D, 1, 2>, 1);
-  } else if (p.num_tokens <= 32 * sms) {
+  } else if (wide >= 4096 && p.num_tokens <= 32 * sms) {
     launch(rope_store_kernel<D, 2, 2>, 2);
+  } else if (wide <= 1024 && p.num_tokens > 16 * sms) {
+    launch(rope_store_kernel<D, 8, 2>, 8);
   } else {
     launch(rope_store_kernel<D, 4, 2>, 4);
   }

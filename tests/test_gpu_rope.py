@@ -85,7 +85,10 @@ def test_a_turn_back_is_the_transpose():
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("t,hq,hkv,d,bs,rot", [(1, 8, 8, 64, 16, 64), (64, 16, 8, 128, 256, 128),
                                                (37, 3, 1, 128, 64, 64), (3001, 4, 2, 64, 32, 32),
-                                               (11, 6, 3, 128, 16, 6), (5, 0, 2, 128, 16, 128)])
+                                               (11, 6, 3, 128, 16, 6), (5, 0, 2, 128, 16, 128),
+                                               # 2, 4, 4 and 8 tokens a CTA
+                                               (901, 28, 2, 128, 64, 128), (903, 2, 1, 128, 64, 96),
+                                               (4801, 30, 1, 128, 256, 64), (2503, 4, 2, 128, 64, 16)])
 def test_rope_store_equals_rope_then_store(t, hq, hkv, d, bs, rot, inter):
     """From slices of one projection; bit for bit, rows no token names untouched."""
     rng = np.random.default_rng(t + hq)
