@@ -10,13 +10,24 @@
 //     hi = e4m3(y), mid = e4m3(y - hi), lo = e4m3(y - hi - mid) (about 2^-13 of an element;
 //     a score's error enters the exponent multiplied by the score's size). Row 3h + t of the
 //     B operand is term t of head h, so a softmax thread reads its 3 G columns in one load.
-//   * the V scale of a block multiplies its probabilities: P'_j = 2^(x_j - m) vs[b] / R, with
-//     R the largest V scale of the item so far (kept by the scheduler warp): one exponential
-//     per (position, head). P' <= 2^kBound; a tile whose maximum would pass it moves the
-//     reference m, and a larger V scale moves R; both rescale O^T in tensor memory.
-//     P' is two e4m3 terms, hi = e4m3(P') and lo = e4m3(128 (P' - hi)) in rows 2h and 2h + 1
-//     (about 2^-8 relative, with an absolute floor of 2^-18 against a largest P' of 2^3 to
-//     2^6); O = (O_hi + O_lo / 128) R / l.
+//   * the V scale of a block multiplies its probabilities, as a logarithm: y_j = x_j +
+//     log2(vs[b]), P'_j = 2^(y_j - u), with the reference u set from the largest product.
+//     (Bounding the two factors apart, by the largest x and the largest V scale, lost the
+//     answer when they belonged to different positions: a large scale that nothing attends to
+//     pushed all weights below the codes' range.) P' <= 2^kBound; a tile that would pass it
+//     moves u and rescales O^T in tensor memory.
+//   * l has a reference m of its own, set with u: m = (largest y) - (largest log2(vs) so far),
+//     never lower than it was. In choosing u a scale counts as 2^-kSpread of the largest one
+//     at least, so that x - m <= kSpread + kBound - kTarget: fp32 holds the sum, and one
+//     maximum a head serves both. (With a second maximum, of x, 256 ragged contexts took 1.7 us
+//     more.)
+//   * P' is three e5m2 terms, hi = e5m2(P'), mid = e5m2(16 (P' - hi)) and lo = e5m2(256 (P' -
+//     hi - mid / 16)) in rows 3h .. 3h + 2 (kind::f8f6f4 takes its operands' formats apart).
+//     Three bits each: 2^-9 of P' from 2^15 down to 2^-14, 2^-8 to 2^-15, and at most 2^-23
+//     below. The largest P' is 2^12 or more when the reference is set, so 2^-27 of the part's
+//     largest product keeps its bits. (Two e4m3 terms reach over 22 bits in all: a position of
+//     weight and no value, as the first one of a context often is, cost the thousands behind
+//     it their weights.) O = (O_hi + O_mid / 16 + O_lo / 256) 2^(u - m) / l.
 //
 // Work. CTAs work in groups of 4, 2 or 1 (the largest that divides the kv heads): the members
 // of a group walk the same tiles of 256 positions for neighbouring kv heads, so rows of
@@ -57,7 +68,6 @@ namespace {
 constexpr int TT = 256;        // positions per tile
 constexpr int TM = 128;        // positions per product
 constexpr int HD = 128;        // head dim
-constexpr int NK = 3;          // K ring (tiles of 32 KB)
 constexpr int NV = 3;          // V ring
 constexpr int ND = 8;          // tile records ahead
 constexpr int QN = 2;          // q slots (one per item in flight)
@@ -76,10 +86,12 @@ constexpr int kTailCost = 4;   // least of a context's last tile
 // equal (10.0 / 10.1), at 1024 four sequences want the split (11.1 / 10.4, 8 q heads 13.0 / 11.3).
 constexpr int kWholeTiles = 2;
 constexpr int kItemCost = 5;   // an item's own (its q terms, first reference and epilogue)
-constexpr float kTarget = 3.f;  // a new reference puts the largest P' at 2^kTarget ...
-constexpr float kBound = 6.f;   // ... and it moves when one would pass 2^kBound (128 (P' - hi)
-                                // is then at most 256, inside e4m3's 448)
-constexpr float kLoScale = 128.f;
+constexpr float kTarget = 12.f;  // a new reference puts the largest P' at 2^kTarget ...
+constexpr float kBound = 15.f;   // ... and it moves when one would pass 2^kBound (the scaled
+                                 // rests of P' are then at most 2^15, inside e5m2's 57344)
+constexpr float kTermScale = 16.f;  // of each term over the one before
+constexpr float kSpread = 80.f;      // octaves of V scales that count in choosing u
+constexpr float kNoScale = -1000.f;  // the largest log2 of a V scale while all have been 0
 constexpr float kLog2eF = 1.4426950408889634f;
 
 constexpr int round_up(int x, int a) { return (x + a - 1) / a * a; }
@@ -87,18 +99,17 @@ constexpr int round_up(int x, int a) { return (x + a - 1) / a * a; }
 struct TileRec {
   int ids[kMaxBlk];
   float ks[kMaxBlk];
-  float vs[kMaxBlk];   // V scale / R
+  float lvs[kMaxBlk];  // log2 of the V scales
+  float lmax;          // the largest one of the item so far
   int n;               // positions of the tile inside the context
   int first;           // first tile of its item
   int last;            // last tile of its item
   int stop;            // no more tiles
   int row_in_blk;      // first row within ids[0] (blocks larger than a tile)
-  float ref;           // R
-  float alpha;         // R of the tile before / R
   int item_s, item_g;  // item: sequence, kv head
   int part, nparts;    // this item's part of the (sequence, kv head)
   int group0;          // group holding part 0
-  int pad[4];
+  int pad[5];
 };
 static_assert(sizeof(TileRec) == 256, "tile record");
 
@@ -111,8 +122,9 @@ static_assert(sizeof(ItemRec) == 32, "item record");
 template <int G>
 struct Cfg {
   static constexpr int NSR = round_up(3 * G, 16);   // rows of q terms (the MMA's N)
-  static constexpr int NPR = round_up(2 * G, 16);   // rows of P terms
-  static constexpr int NP = G > 8 ? 2 : 3;          // P buffers
+  static constexpr int NPR = round_up(3 * G, 16);   // rows of P terms
+  static constexpr int NP = G == 8 ? 2 : 3;         // P buffers
+  static constexpr int NK = G > 8 ? 2 : 3;          // K ring (tiles of 32 KB)
   static constexpr int NS = 4;                      // S buffers in tensor memory
   static constexpr int kQBytes = NSR * 128;
   static constexpr int kPChunk = NPR * 128;         // P terms of 128 positions
@@ -125,7 +137,7 @@ struct Cfg {
   static constexpr int kOffRed = kOffRec + ND * static_cast<int>(sizeof(TileRec));
   // [2][G][8] maxima, [8][G] sums
   static constexpr int kOffQs = round_up(kOffRed + 3 * 8 * G * 4, 16);
-  static constexpr int kEpiBytes = 32 + 36 * 4;  // item record, m and l per head, R
+  static constexpr int kEpiBytes = 32 + 64 * 4;  // item record, m, l and two factors per head
   static constexpr int kOffEpi = round_up(kOffQs + QN * G * 4, 16);
   // heads shared by several epilogue warps meet here when parts are merged
   static constexpr int kOffMerge = round_up(kOffEpi + NO * kEpiBytes, 16);
@@ -186,10 +198,10 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// The first 3 G (scores) or 2 G (outputs) fp32 columns at taddr, rounded up to a load's size.
+// The first 3 G fp32 columns at taddr, rounded up to a load's size.
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float (&v)[N]) {
-  static_assert(N == 2 || N == 4 || N == 8 || N == 16 || N == 32 || N == 48, "columns");
+  static_assert(N == 4 || N == 8 || N == 16 || N == 32 || N == 48, "columns");
   if constexpr (N <= 16) {
     tmem_ld_cols<N>(taddr, v);
   } else {
@@ -205,15 +217,10 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float (&v)[N]) {
     }
   }
 }
-constexpr int load_cols(int n) { return n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 48; }
+constexpr int load_cols(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 48; }
 
-template <int N>
-__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const float (&v)[N]) {
-  if constexpr (N == 16) tmem_st16(taddr, v);
-  else tmem_st32(taddr, v);
-}
-
-// One merge step over cnt <= kFan parts by the four epilogue warps; part i's record is at slot
+// One merge step over cnt <= kFan parts by the four epilogue warps. A part's record is its own
+// attention output (divided by its sum) with its maximum and sum; part i's is at slot
 // first + i * step, but part 0's at `slot0`. A warp takes whole heads (G >= 4) or a head's
 // parts in turn with 4 / G - 1 other warps. Lane i reads part i's maximum and sum; the lanes
 // hold 4 output dims each, so a part's row is one 16-byte load per lane, and all of a head's
@@ -242,8 +249,8 @@ __device__ __forceinline__ void merge_parts(float* ws_o, float* ws_ml, int cnt, 
         o[i] = __ldcg(reinterpret_cast<const float4*>(ws_o + (slot_of(i * S + sub) * G + h) * HD) + lane);
     }
     const float M = warp_max(ml.x);
-    const float f = M > -INFINITY ? ex2_approx(ml.x - M) : 0.f;
-    float L = __fmul_rn(ml.y, f);
+    const float f = M > -INFINITY ? __fmul_rn(ml.y, ex2_approx(ml.x - M)) : 0.f;
+    float L = f;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L = __fadd_rn(L, __shfl_xor_sync(0xffffffffu, L, off));
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -270,10 +277,11 @@ __device__ __forceinline__ void merge_parts(float* ws_o, float* ws_ml, int cnt, 
       named_bar_sync(2, 128);  // before the buffer's next use
     }
     if (sub == 0) {
+      const float r = __fdividef(1.f, L);
+      A = make_float4(A.x * r, A.y * r, A.z * r, A.w * r);
       if (out) {
-        const float r = __fdividef(1.f, L);
         *reinterpret_cast<uint2*>(out + h * HD + 4 * lane) =
-            make_uint2(pack_bf16x2(A.x * r, A.y * r), pack_bf16x2(A.z * r, A.w * r));
+            make_uint2(pack_bf16x2(A.x, A.y), pack_bf16x2(A.z, A.w));
       } else {
         const int64_t to = static_cast<int64_t>(slot0) * G + h;
         reinterpret_cast<float4*>(ws_o + to * HD)[lane] = A;
@@ -290,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              const __grid_constant__ CUtensorMap tmKt,
                              const __grid_constant__ CUtensorMap tmVt, const BsParams p) {
   using C = Cfg<G>;
-  constexpr int NS = C::NS, NP = C::NP, NSR = C::NSR, NPR = C::NPR;
+  constexpr int NS = C::NS, NP = C::NP, NK = C::NK, NSR = C::NSR, NPR = C::NPR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -505,9 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* ring = smem + (is_v ? C::kOffV : C::kOffK);
     uint64_t* full = is_v ? v_full : k_full;
     uint64_t* empty = is_v ? v_empty : k_empty;
-    static_assert(NK == NV, "one ring depth");
     constexpr uint32_t idS = idesc_e4m3_f32(TM, NSR, 0, 0);  // K K-major, q terms K-major
-    constexpr uint32_t idO = idesc_e4m3_f32(HD, NPR, 1, 0);  // V^T MN-major, P terms K-major
+    // V^T MN-major, P terms (e5m2) K-major
+    constexpr uint32_t idO = idesc_e4m3_e5m2_f32(HD, NPR, 1, 0);
     const uint64_t ring_desc = smem_desc_sw128(smem_u32(ring), is_v ? kHalf : 16, 1024);
     const uint64_t b_desc = smem_desc_sw128(smem_u32(smem + (is_v ? C::kOffP : C::kOffQ)), 16, 1024);
     const int rows_log2 = bs < TT ? p.bs_log2 : 8;   // rows per box of a full tile
@@ -517,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ended = false;                   // the stop record was seen
     // load of tile jl (false: no record yet, or no free slot)
     auto load = [&]() -> bool {
-      const int rs = jl % ND, slot = jl % NK;
+      const int rs = jl % ND, slot = is_v ? jl % NV : jl % NK, lap = is_v ? jl / NV : jl / NK;
       if (!__all_sync(0xffffffffu,
                       mbar_test_wait(&rec_full[rs], (jl / ND) & 1) &&
-                          (jl < NK || mbar_test_wait(&empty[slot], ((jl / NK) - 1) & 1))))
+                          (lap == 0 || mbar_test_wait(&empty[slot], (lap - 1) & 1))))
         return false;
       const TileRec& rec = recs[rs];
       if (rec.stop) {
@@ -632,9 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Before the CTA ends: every copy this warp started has landed (per slot only its last one
     // can still be in flight), every product it issued has finished.
     if (lane == 0) {
+      const unsigned depth = is_v ? NV : NK;
 #pragma unroll 1
-      for (unsigned t = jl > NK ? jl - NK : 0; t < jl; ++t)
-        mbar_wait(&full[t % NK], (t / NK) & 1, p.err);
+      for (unsigned t = jl > depth ? jl - depth : 0; t < jl; ++t)
+        mbar_wait(&full[t % depth], (t / depth) & 1, p.err);
     }
     __syncwarp();
     tc_commit(&mma_drain[is_v]);
@@ -655,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int upto = static_cast<int>((run_end - it.cum + kTileCost - 1) / kTileCost);
       const int tb = tiles < upto || whole ? tiles : upto;
       more = it.cum + it.cost < run_end;
-      float ref = 0.f;
-      float ksc = 0.f, vsc = 0.f;
+      float lmax = kNoScale;
+      float ksc = 0.f, lvs = 0.f;
       bool fresh = true;  // the batch's scales have not been read
       for (int t = ta; t < tb; ++t) {
         const int slot = j % ND;
@@ -695,25 +704,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           fresh = false;
           const int64_t at = static_cast<int64_t>(bid) * p.num_kv_heads + g;
           ksc = __ldg(p.k_scales + at);
-          vsc = __ldg(p.v_scales + at);
+          lvs = __log2f(__ldg(p.v_scales + at));
         }
         const bool used = mine && ((b0 + lane - l0) << p.bs_log2) < it.ctx;
-        const float now = fmaxf(ref, warp_max(used ? vsc : 0.f));
+        lmax = fmaxf(lmax, warp_max(used ? lvs : kNoScale));
         if (mine) {
           rec.ks[lane - l0] = ksc;
-          rec.vs[lane - l0] = now > 0.f ? __fdividef(vsc, now) : 0.f;
+          rec.lvs[lane - l0] = lvs;
         }
         if (lane == 0) {
+          rec.lmax = lmax;
           if (t == tb - 1) {  // what the epilogue needs
             const int group0 = group_of(it.cum);
             rec.group0 = group0;
             rec.part = group - group0;
             rec.nparts = whole ? 1 : group_of(it.cum + (tiles - 1) * kTileCost) - group0 + 1;
           }
-          rec.ref = now;
-          rec.alpha = (t == ta || now == ref || ref == 0.f) ? 1.f : __fdividef(ref, now);
         }
-        ref = now;
         __syncwarp();
         if (lane == 0) mbar_arrive(&scl_full[slot]);
         ++j;
@@ -801,13 +808,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int SC = load_cols(3 * G);
     unsigned j = 0;
     int k = 0;
-    float m[G], l[G], fs[G];
+    float m[G], l[G], u[G], fs[G];
+    auto restart = [&]() {  // for an item's first tile: any reference is above these
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      m[h] = 0.f;
-      l[h] = 0.f;
-      fs[h] = 0.f;
-    }
+      for (int h = 0; h < G; ++h) {
+        m[h] = u[h] = -INFINITY;
+        l[h] = 0.f;
+      }
+    };
+    restart();
+#pragma unroll
+    for (int h = 0; h < G; ++h) fs[h] = 0.f;
     bool failed = false;
     while (true) {
       const int rs = j % ND, sb = j % NS;
@@ -816,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool stop = rec.stop != 0;
       float x[G];
       bool valid = false, first = false, exceeds = false;
-      float vrel = 0.f;
+      float lvs = 0.f, lc = 0.f, lmax = 0.f;
       // warp-uniform: the loads below are warp-wide
       const bool go = __all_sync(0xffffffffu, !failed && !stop);
       if (go) {
@@ -830,7 +841,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < G; ++h) fs[h] = p.scale_log2 * qscale[qs * G + h];
         }
         const float ksc = rec.ks[blk];
-        vrel = valid ? rec.vs[blk] : 0.f;
+        lvs = valid ? rec.lvs[blk] : 0.f;
+        lmax = rec.lmax;
+        lc = fmaxf(lvs, lmax - kSpread);
         failed |= !wait_or_abort(&s_full[sb], (j / NS) & 1, p.err, abort_flag, wl);
         tc_fence_after();
         float sv[SC];
@@ -844,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < G; ++h) {
           const float d = (sv[3 * h] + sv[3 * h + 1]) + sv[3 * h + 2];
           x[h] = valid ? d * (fs[h] * ksc) : -INFINITY;
-          exceeds |= x[h] > m[h] + kBound;
+          exceeds |= x[h] > u[h] + (kBound - lc);
         }
       }
       // One vote a tile: nothing to do (the reference holds for every position), or the
@@ -856,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (go) {
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float v = warp_max(x[h]);
+            const float v = warp_max(x[h] + lc);
             if (lane == 0) rb[h * 8 + warp] = v;
           }
         }
@@ -874,35 +887,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < G; ++h) {
           const float4 w0 = *reinterpret_cast<const float4*>(rb + h * 8);
           const float4 w1 = *reinterpret_cast<const float4*>(rb + h * 8 + 4);
-          const float mx = fmaxf(fmax3(fmaxf(w0.x, w0.y), w0.z, w0.w),
+          const float my = fmaxf(fmax3(fmaxf(w0.x, w0.y), w0.z, w0.w),
                                  fmax3(fmaxf(w1.x, w1.y), w1.z, w1.w));
-          alpha[h] = 1.f;
-          if (first) {
-            m[h] = mx - kTarget;
-            l[h] = 0.f;
-          } else if (mx > m[h] + kBound) {
-            const float mn = mx - kTarget;
-            alpha[h] = ex2_approx(m[h] - mn);
-            l[h] *= alpha[h];
-            m[h] = mn;
-            moved = true;
-          }
+          // without branches (with them: 47.5 us, not 42, at 16 heads a kv head)
+          const bool passed = my > u[h] + kBound;
+          const float un = passed ? my - kTarget : u[h], mn = fmaxf(m[h], my - lmax);
+          alpha[h] = ex2_approx(u[h] - un);
+          l[h] *= ex2_approx(m[h] - mn);
+          u[h] = un;
+          m[h] = mn;
+          moved |= passed;
         }
+        moved = moved && !first;  // a first tile's product overwrites O
       }
       // from here the record is known to be sound for every thread
       if (first && tid == 0) mbar_arrive(&q_empty[k % QN]);  // every thread has its q scales
       const int n = rec.n;
       const bool last = rec.last != 0;
-      const float av = rec.alpha;
-      bool rescale = moved || av != 1.f;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float e = valid ? ex2_approx(x[h] - m[h]) : 0.f;
-        l[h] += e;
-        pp[h] = e * vrel;
-        alpha[h] = moved ? alpha[h] * av : av;
+        l[h] += ex2_approx(x[h] - m[h]);  // x is -inf past the context
+        pp[h] = ex2_approx((x[h] + lvs) - u[h]);
       }
-      if (first) rescale = false;  // O is overwritten by the item's first product
       // this P buffer was last read by the value product of tile j - NP
       const int pb = j % NP;
       if (j >= NP)
@@ -910,15 +916,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         uint8_t* pt = smem + C::kOffP + pb * C::kPBytes + sg * C::kPChunk + (r & 15);
         const int c = r >> 4;
+        auto put = [&](int row, uint32_t code) {
+          pt[row * 128 + (((c ^ row) & 7) << 4)] = static_cast<uint8_t>(code);
+        };
 #pragma unroll
         for (int h = 0; h < G; h += 2) {
-          uint32_t hi, lo;
-          split_e4m3x2(pp[h], h + 1 < G ? pp[h + 1] : 0.f, kLoScale, hi, lo);
+          float2 rest = make_float2(pp[h], h + 1 < G ? pp[h + 1] : 0.f);
 #pragma unroll
-          for (int e = 0; e < 2 && h + e < G; ++e) {
-            const int row = 2 * (h + e);
-            pt[row * 128 + (((c ^ row) & 7) << 4)] = static_cast<uint8_t>(hi >> (8 * e));
-            pt[(row + 1) * 128 + (((c ^ (row + 1)) & 7) << 4)] = static_cast<uint8_t>(lo >> (8 * e));
+          for (int term = 0; term < 3; ++term) {
+            float2 held;
+            const uint32_t code = e5m2x2(rest.x, rest.y, held);
+            put(3 * h + term, code);
+            if (h + 1 < G) put(3 * h + 3 + term, code >> 8);
+            rest = make_float2((rest.x - held.x) * kTermScale, (rest.y - held.y) * kTermScale);
           }
         }
       }
@@ -933,27 +943,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
         }
       }
-      if (sg == 0 && rescale) {
+      if (sg == 0 && moved) {
         // uniform over the group; O holds the products up to tile j - 1
         const unsigned t = j - 1;
         failed |= !wait_or_abort(&pv_done[t % NP], (t / NP) & 1, p.err, abort_flag, wl);
         tc_fence_after();
-        constexpr int OC = NPR;  // 16 or 32 columns, 2 per head
-        float o[OC];
-        const uint32_t at = tmem + C::kTmemO + (k % NO) * NPR + lane_off;
-        tmem_ld_n<OC>(at, o);
-        tc_wait_ld();
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-          o[2 * h] *= alpha[h];
-          o[2 * h + 1] *= alpha[h];
+        for (int c = 0; c < NPR; c += 16) {  // three columns per head
+          float o[16];
+          const uint32_t at = tmem + C::kTmemO + (k % NO) * NPR + c + lane_off;
+          tmem_ld16(at, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + i < 3 * G) o[i] *= alpha[(c + i) / 3];
+          tmem_st16(at, o);
         }
-        tmem_st_n<OC>(at, o);
         tc_wait_st();
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      const float ref = rec.ref;
       const ItemRec it{rec.item_s, rec.item_g, rec.part, rec.nparts, rec.group0, 0, {0, 0}};
       __syncwarp();
       if (lane == 0) {
@@ -962,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++j;
       if (last) {
-        // hand the item to the epilogue: l over the 256 positions, m, R
+        // hand the item to the epilogue: l over the 256 positions, m, the outputs' factors
         float* lb = red + 2 * 8 * G;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -972,26 +981,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) lb[warp * G + h] = v;
         }
         named_bar_sync(1, kSoftThreads);
-        if (tid == 0) {
+        if (warp == 0) {  // a lane per head
           const int b = k % NO;
           if (k >= NO)
             failed |= !wait_or_abort(&epi_empty[b], ((k / NO) - 1) & 1, p.err, abort_flag, wl);
-          if (!failed) {
+          if (__all_sync(0xffffffffu, !failed)) {
             uint8_t* es = smem + C::kOffEpi + b * C::kEpiBytes;
-            *reinterpret_cast<ItemRec*>(es) = it;
-            float* em = reinterpret_cast<float*>(es + 32);
+            if (lane == 0) *reinterpret_cast<ItemRec*>(es) = it;
+            float mine = 0.f, shift = 0.f;
 #pragma unroll
             for (int h = 0; h < G; ++h) {
+              mine = lane == h ? m[h] : mine;
+              shift = lane == h ? u[h] - m[h] : shift;
+            }
+            if (lane < G) {
               float L = 0.f;
 #pragma unroll
-              for (int w = 0; w < 8; ++w) L += lb[w * G + h];
-              em[h] = m[h];
-              em[16 + h] = L;
+              for (int w = 0; w < 8; ++w) L += lb[w * G + lane];
+              // O's factor 2^(u - m) / l in two, which stay in fp32's range
+              const float half = ex2_approx(0.5f * shift);
+              float* em = reinterpret_cast<float*>(es + 32) + lane;
+              em[0] = mine;
+              em[16] = L;
+              em[32] = __fdividef(half, L);
+              em[48] = half;
             }
-            em[32] = ref;
-            mbar_arrive(&epi_full[b]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&epi_full[b]);
           }
         }
+        restart();
         ++k;
       }
     }
@@ -1018,13 +1037,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool failed = !wait_or_abort(&epi_full[b], (k / NO) & 1, p.err, abort_flag, wl);
       const uint8_t* es = smem + C::kOffEpi + b * C::kEpiBytes;
       const ItemRec it = *reinterpret_cast<const ItemRec*>(es);
-      float m[G], L[G];
+      float m[G], L[G], f0[G], f1[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        m[h] = reinterpret_cast<const float*>(es + 32)[h];
-        L[h] = reinterpret_cast<const float*>(es + 32)[16 + h];
+        const float* em = reinterpret_cast<const float*>(es + 32) + h;
+        m[h] = em[0];
+        L[h] = em[16];
+        f0[h] = em[32];
+        f1[h] = em[48];
       }
-      const float ref = reinterpret_cast<const float*>(es + 32)[32];
       // part i of an item lives in CTA (group0 + i, member): a CTA's first item in slot 0 when
       // it began in an earlier group, its last item in slot 1 when it goes on in a later one
       auto slot_of = [&](int i) -> int64_t {
@@ -1039,7 +1060,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (leader) mbar_arrive(&epi_empty[b]);
       if (it.stop) break;
       const bool finish = it.nparts == 2 && *last_flag != 0;
-      float wo[G], po[G];  // this part's weight, the other one's row times its weight
+      // this part's weight and the parts' sum, the other one's row times its weight
+      float wo[G], sum[G], po[G];
       if (finish) {
         const int64_t at = slot_of(it.part ^ 1) * G;
         float2 ml[G];
@@ -1051,20 +1073,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float mx = fmaxf(m[h], ml[h].x);
-          const float f = ex2_approx(ml[h].x - mx);
-          wo[h] = ex2_approx(m[h] - mx);
-          L[h] = __fadd_rn(__fmul_rn(L[h], wo[h]), __fmul_rn(ml[h].y, f));
+          const float f = __fmul_rn(ml[h].y, ex2_approx(ml[h].x - mx));
+          wo[h] = __fmul_rn(L[h], ex2_approx(m[h] - mx));
+          sum[h] = __fadd_rn(wo[h], f);
           po[h] = fmaf(po[h], f, 0.f);  // as in merge_parts, never -0
         }
       }
       failed |= !wait_or_abort(&o_full[b], (k / NO) & 1, p.err, abort_flag, wl);
       tc_fence_after();
-      constexpr int OC = load_cols(2 * G);
+      constexpr int OC = load_cols(3 * G);
       float oc[OC], o[G];
       tmem_ld_n<OC>(tmem + C::kTmemO + b * NPR + lane_off, oc);
       tc_wait_ld();
 #pragma unroll
-      for (int h = 0; h < G; ++h) o[h] = fmaf(oc[2 * h + 1], 1.f / kLoScale, oc[2 * h]) * ref;
+      for (int h = 0; h < G; ++h) {
+        const float sum = fmaf(fmaf(oc[3 * h + 2], 1.f / kTermScale, oc[3 * h + 1]), 1.f / kTermScale, oc[3 * h]);
+        o[h] = sum * f0[h] * f1[h];
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[b]);
@@ -1072,13 +1097,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.nparts == 1 || finish) {
         if (finish) {
 #pragma unroll
-          for (int h = 0; h < G; ++h) o[h] = __fadd_rn(fmaf(wo[h], o[h], 0.f), po[h]);
+          for (int h = 0; h < G; ++h)
+            o[h] = __fadd_rn(fmaf(wo[h], o[h], 0.f), po[h]) * __fdividef(1.f, sum[h]);
           if (leader) *reinterpret_cast<volatile unsigned long long*>(p.counters + 2 * slot_of(0)) = 0ull;
         }
         if (!failed) {
 #pragma unroll
           for (int h = 0; h < G; ++h)
-            p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(o[h] * __fdividef(1.f, L[h]));
+            p.out[(row0 + h) * HD + dl] = __float2bfloat16_rn(o[h]);
         }
       } else {
         const int64_t mine = slot_of(it.part);

@@ -164,6 +164,14 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b, float2& back) {
   return static_cast<uint32_t>(c);
 }
 
+// The same for e5m2 (saturated to +-57344); an e5m2 code is the upper byte of an fp16 number.
+__device__ __forceinline__ uint32_t e5m2x2(float a, float b, float2& back) {
+  const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
+  const uint32_t h = __byte_perm(c, 0u, 0x1404);
+  back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return c;
+}
+
 // hi / lo e4m3 terms of two values: hi = e4m3(v), lo = e4m3(lo_scale * (v - hi)),
 // as two packed byte pairs (value a in the low byte of each).
 __device__ __forceinline__ void split_e4m3x2(float a, float b, float lo_scale, uint32_t& hi,

@@ -407,6 +407,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn_maj
          (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
+// The same with an e5m2 B operand.
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N, int a_mn_major,
+                                                           int b_mn_major) {
+  return idesc_e4m3_f32(M, N, a_mn_major, b_mn_major) | (1u << 10);
+}
 
 // ----------------------------------------------------------------- math
 __device__ __forceinline__ float ex2_approx(float x) {
