@@ -543,12 +543,12 @@ pa_status pa_rope_store_kvcache_fp8_blockscale(
  * pa_decode_fp8_blockscale — pa_decode over e4m3 pools with block scales: one query token
  * per sequence attends over the values the pools hold (code * scale; a scale is 0 or any
  * fp32 from 2^-126 up to where 448 * scale still is finite). The tensor cores read the codes
- * as they are stored; q reaches them as three e4m3 terms (about 2^-13 relative per element),
- * the probabilities, times their block's V scale, as three e5m2 terms: the product of a
- * position's probability and V scale is held to 2^-9 of itself (2^-8 in the last octave) down
- * to 2^-27 of the largest such product in its part of the context; what lies below is off by
- * at most 2^-35 of that largest product. (V scales count as at least 2^-80 of the largest one
- * here.) The sum of the probabilities is fp32.
+ * as they are stored; q reaches them as three e4m3 terms (exact down to 2^-18 of the head's
+ * largest element, below off by at most 2^-25 of that one), the probabilities, times their
+ * block's V scale, as three e5m2 terms: the product of a position's probability and V scale is
+ * held to 2^-9 of itself (2^-8 in the last octave) down to 2^-27 of the largest such product in
+ * its part of the context; what lies below is off by at most 2^-35 of that largest product. (V
+ * scales count as at least 2^-80 of the largest one here.) The sum of the probabilities is fp32.
  * The context is split over the SMs evenly, whatever the lengths; no partition size.
  *   out, q          [num_seqs, Hq, D] bf16; a sequence with context_lens[s] <= 0 gets zeros.
  *   max_context_len host upper bound of context_lens; a larger device value is clipped to

@@ -6,10 +6,13 @@
 //   l = sum_j 2^(x_j - m). The tensor cores multiply the stored codes themselves
 //   (kind::f8f6f4, fp32 accumulation): S = K Q^T per 128 positions (M = positions, N = rows
 //   of q terms) and O^T += V^T P^T (M = head dims, N = rows of P terms).
-//   * q (bf16) is three e4m3 terms of one fp32 scale per head, y = q * 448 / amax:
-//     hi = e4m3(y), mid = e4m3(y - hi), lo = e4m3(y - hi - mid) (about 2^-13 of an element;
-//     a score's error enters the exponent multiplied by the score's size). Row 3h + t of the
-//     B operand is term t of head h, so a softmax thread reads its 3 G columns in one load.
+//   * q (bf16) is three e4m3 terms of one power of two per head, y = q 2^-k with the head's
+//     largest |y| in (224, 448]: hi = e4m3(y), mid = e4m3(16 (y - hi)), lo = e4m3(2^22 (y - hi -
+//     mid / 16)). A power of two leaves bf16's 8 bits as they are: hi and mid hold them where
+//     hi is normal, lo what hi's and mid's steps leave of smaller elements. So q is exact down
+//     to 2^-18 of the head's largest element, and off by at most 2^-25 of that one below. Row
+//     3h + t of the B operand is term t of head h, so a softmax thread reads its 3 G columns in
+//     one load.
 //   * the V scale of a block multiplies its probabilities, as a logarithm: y_j = x_j +
 //     log2(vs[b]), P'_j = 2^(y_j - u), with the reference u set from the largest product.
 //     (Bounding the two factors apart, by the largest x and the largest V scale, lost the
@@ -90,6 +93,7 @@ constexpr float kTarget = 12.f;  // a new reference puts the largest P' at 2^kTa
 constexpr float kBound = 15.f;   // ... and it moves when one would pass 2^kBound (the scaled
                                  // rests of P' are then at most 2^15, inside e5m2's 57344)
 constexpr float kTermScale = 16.f;  // of each term over the one before
+constexpr float kQLoScale = 4194304.f;  // 2^22: of q's third term
 constexpr float kSpread = 80.f;      // octaves of V scales that count in choosing u
 constexpr float kNoScale = -1000.f;  // the largest log2 of a V scale while all have been 0
 constexpr float kLog2eF = 1.4426950408889634f;
@@ -768,8 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f0 = bf16lo_to_f32(raw[h].x), f1 = bf16hi_to_f32(raw[h].x);
           const float f2 = bf16lo_to_f32(raw[h].y), f3 = bf16hi_to_f32(raw[h].y);
           const float amax = warp_max(fmaxf(fmaxf(fabsf(f0), fabsf(f1)), fmaxf(fabsf(f2), fabsf(f3))));
-          float inv = 448.f / amax;
-          if (!(inv <= FLT_MAX)) inv = 0.f;  // all zero (or tiny): codes 0, scale 0
+          // the smallest k >= -126 with amax <= 448 2^k (448 = 1.75 2^8)
+          const unsigned bits = __float_as_uint(amax);
+          const int up = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+          const int e = up > -126 ? up : -126;
+          const float inv = __uint_as_float(static_cast<unsigned>(127 - e) << 23);
           float y[4] = {f0 * inv, f1 * inv, f2 * inv, f3 * inv};
 #pragma unroll
           for (int term = 0; term < 3; ++term) {
@@ -779,12 +786,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t c23 = e4m3x2(y[2], y[3], b23);
             *reinterpret_cast<uint32_t*>(qd + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
                                          (lane & 3) * 4) = c01 | (c23 << 16);
-            y[0] -= b01.x;
-            y[1] -= b01.y;
-            y[2] -= b23.x;
-            y[3] -= b23.y;
+            const float by = term == 0 ? kTermScale : kQLoScale / kTermScale;
+            y[0] = (y[0] - b01.x) * by;
+            y[1] = (y[1] - b01.y) * by;
+            y[2] = (y[2] - b23.x) * by;
+            y[3] = (y[3] - b23.y) * by;
           }
-          if (lane == 0) qscale[qs * G + h] = inv > 0.f ? amax / 448.f : 0.f;
+          // an infinite element makes its head's scores NaN
+          if (lane == 0)
+            qscale[qs * G + h] = amax <= FLT_MAX ? __uint_as_float(static_cast<unsigned>(127 + e) << 23) : NAN;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -855,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         exceeds = first;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          const float d = (sv[3 * h] + sv[3 * h + 1]) + sv[3 * h + 2];
+          const float d = fmaf(sv[3 * h + 2], 1.f / kQLoScale, fmaf(sv[3 * h + 1], 1.f / kTermScale, sv[3 * h]));
           x[h] = valid ? d * (fs[h] * ksc) : -INFINITY;
           exceeds |= x[h] > u[h] + (kBound - lc);
         }

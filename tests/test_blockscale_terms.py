@@ -62,3 +62,37 @@ def test_the_sum_s_terms_stay_in_fp32():
     """x - m <= spread + bound - target = 83 octaves, and at most 2^30 positions."""
     spread = 80
     assert spread + BOUND - TARGET + 30 + math.log2(2) < 127
+
+
+# ------------------------------------------------------------------------------ q
+def q_terms(q):
+    """The value that the three e4m3 terms of a head's elements (bf16 numbers) stand for."""
+    from oracle.fp8_block import LUT, encode, needed_scale
+    s = needed_scale(q)                      # a power of two
+    y = q / s
+    hi = LUT[encode(y)]
+    mid = LUT[encode(16.0 * (y - hi))]
+    lo = LUT[encode(2.0 ** 22 * (y - hi - mid / 16.0))]
+    return (hi + mid / 16.0 + lo / 2.0 ** 22) * s
+
+
+def bf16(x):
+    """Nearest bf16 number: 8 bits, and no step below 2^-133."""
+    _, e = np.frexp(x)
+    step = np.ldexp(1.0, np.maximum(e - 8, -133))
+    return np.rint(x / step) * step
+
+
+def test_q_is_exact_down_to_2_to_the_minus_18_of_its_largest_element():
+    rng = np.random.default_rng(3)
+    for top in (1.0, 448.0, 449.0, 1.7421875, 3.0e-5, 1.0e30, 2.0 ** -120):
+        top = float(bf16(np.array(top)))
+        x = bf16(top * 2.0 ** rng.uniform(-18, 0, 50000) * rng.choice([-1.0, 1.0], 50000))
+        x = np.append(x[np.abs(x) >= 2.0 ** -18 * top], top)
+        assert np.array_equal(q_terms(x), x)
+
+
+def test_smaller_elements_of_q_are_off_by_2_to_the_minus_25_of_the_largest():
+    rng = np.random.default_rng(4)
+    x = np.append(bf16(2.0 ** rng.uniform(-60, -18, 100000) * rng.choice([-1.0, 1.0], 100000)), 1.0)
+    assert np.all(np.abs(q_terms(x) - x) <= 2.0 ** -25)

@@ -103,3 +103,37 @@ def test_scales_at_the_ends_of_the_range(exponent):
         err = np.abs(got[s] - ref[s]).max()
         assert err <= 2.0 ** -7 * np.abs(ref[s]).max() + 2.0 ** -133
     assert pa.pa_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("g", [1, 4, 16])
+@pytest.mark.parametrize("octaves", [8, 14, 17])
+def test_a_query_s_small_elements_beside_a_large_one(g, octaves):
+    """One element is 2^octaves above the others and meets keys that are zero there: the scores
+    are those of the small ones."""
+    c = Case([1500, 300], 2 * g, 2, 64, seed=octaves, spread=0.3)
+    q = bf16_bits_to_f64(c.q) * 3.0
+    q[..., 17] = 2.0 ** octaves * 3.3
+    c.q = f32_to_bf16_bits(q.astype(np.float32))
+    c.kc[..., 17] = 0
+    close_each(c, f"G {g}, 2^{octaves}")
+
+
+@pytest.mark.parametrize("exponent", [-130, -100, 60])
+def test_queries_of_any_size(exponent):
+    """q and the K scales cancel, as far as the scales' range goes."""
+    c = Case([900, 70], 8, 2, 64, seed=5, spread=0.2)
+    q = np.ldexp(bf16_bits_to_f64(c.q), exponent)
+    c.q = f32_to_bf16_bits(q.astype(np.float32))
+    ok = ~np.isnan(c.ks)
+    c.ks[ok] = np.ldexp(c.ks[ok], min(-exponent, 120))
+    close_each(c, f"2^{exponent}")
+
+
+def test_an_infinite_query_element_stays_in_its_head():
+    c = Case([700, 40], 4, 2, 64, seed=6)
+    ok = to_f64(c.gpu())
+    c.dev[0][0, 1, 5] = float("inf")
+    got = to_f64(c.gpu())
+    assert np.isnan(got[0, 1]).all()
+    got[0, 1] = ok[0, 1]
+    assert np.array_equal(got, ok)
