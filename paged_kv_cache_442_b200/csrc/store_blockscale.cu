@@ -398,7 +398,9 @@ __device__ __forceinline__ void append_few(const AppendParams& p, const Span& u,
     return;
   }
   float* scale_at = (is_v ? p.v_scales : p.k_scales) + static_cast<int64_t>(u.id) * p.num_kv_heads + g;
-  const float old = u.r0 ? __ldcg(scale_at) : 0.f;
+  // read by the lane that writes it below, so that no other lane can see the new one
+  float old = 0.f;
+  if (lane == 0 && u.r0) old = __ldcg(scale_at);
   if (turned) {
     unsigned long long rate[8];
 #pragma unroll
@@ -415,6 +417,7 @@ __device__ __forceinline__ void append_few(const AppendParams& p, const Span& u,
     }
   }
   const unsigned amax = __reduce_max_sync(0xffffffffu, top_of(a, b));
+  old = __shfl_sync(0xffffffffu, old, 0);
   const float need = exp2_int(scale_exponent(amax));
   const float scale = old >= need ? old : need;  // old is 0 for a block that starts here
   const float inv = __frcp_rn(scale);
