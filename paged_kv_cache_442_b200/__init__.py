@@ -167,7 +167,8 @@ _native_module = None
 
 def _native():
     """The compiled marshalling of the rotary and block-scale entry points (loaded once):
-    checks the tensors and calls libpa.so. Raises if it is missing: there is no fallback."""
+    checks the tensors and calls libpa.so. Raises if it is missing or was built for another
+    torch or Python (its tensors' layout may be another): there is no fallback."""
     global _native_module
     if _native_module is None:
         import importlib.machinery
@@ -177,6 +178,10 @@ def _native():
         if not os.path.exists(BINDING_PATH):
             raise ImportError(f"{BINDING_PATH} not found: build it with "
                               "`python -m paged_kv_cache_442_b200.build`")
+        from . import build
+        if build.built_for() != build.binding_target():
+            raise ImportError(f"{BINDING_PATH} was built for {build.built_for() or 'an unknown torch'}, this is "
+                              f"{build.binding_target()}: build it with `python -m paged_kv_cache_442_b200.build`")
         loader = importlib.machinery.ExtensionFileLoader("_pa_torch", BINDING_PATH)
         spec = importlib.util.spec_from_loader("_pa_torch", loader)
         module = importlib.util.module_from_spec(spec)

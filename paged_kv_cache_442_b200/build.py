@@ -5,14 +5,18 @@ Each .cu (device and host code) and .cpp (host-only code) under csrc/ is compile
 an object in _build/ by nvcc (in parallel), then the
 objects are linked into paged_kv_cache_442_b200/libpa.so with the CUDA runtime
 linked statically. csrc/torch/binding.cpp (torch tensors to C pointers, for the Python
-binding) becomes _pa_torch.so, linked against libpa.so and torch. Rebuilds only when a source
-or header is newer than the libraries.
+binding) becomes _pa_torch.so, linked against libpa.so and torch; it holds the names of the torch
+and the Python it was built for. Without torch only libpa.so is built. Rebuilds only when a
+source or header is newer than the libraries, or torch or Python are others.
 """
 from __future__ import annotations
 
 import argparse
 import glob
+import importlib.metadata
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -58,8 +62,35 @@ def _binding_deps():
     return [BINDING_SRC, os.path.abspath(__file__)] + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def binding_target() -> str | None:
+    """The torch and the Python that _pa_torch.so has to be built for; None without torch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = torch.__version__
+    return f"torch {version}, Python {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def built_for() -> str | None:
+    """What the _pa_torch.so that is there was built for (read, not loaded: a module of another
+    torch may not load); None if it does not say."""
+    if not os.path.exists(BINDING):
+        return None
+    with open(BINDING, "rb") as f:
+        name = re.search(rb"pa_built_for{([^}]*)}", f.read())
+    return name.group(1).decode() if name else None
+
+
+def _binding_up_to_date() -> bool:
+    target = binding_target()
+    return target is None or (built_for() == target and _newer_than(BINDING, _binding_deps()))
+
+
 def up_to_date() -> bool:
-    return _newer_than(LIB, _deps()) and _newer_than(BINDING, _binding_deps())
+    return _newer_than(LIB, _deps()) and _binding_up_to_date()
 
 
 def _compile_binding() -> str:
@@ -73,6 +104,7 @@ def _compile_binding() -> str:
     obj = os.path.join(BUILD_DIR, "binding.cpp.o")
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DPA_BUILT_FOR="{binding_target()}"',
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-I", INCLUDE,
            "-c", BINDING_SRC, "-o", obj]
@@ -112,8 +144,8 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 8) -> st
         return src, obj, r
 
     with ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = None if not force and _newer_than(BINDING, _binding_deps()) else \
-            ex.submit(_compile_binding)
+        wanted = binding_target() is not None and (force or not _binding_up_to_date())
+        binding = ex.submit(_compile_binding) if wanted else None
         results = [] if not force and _newer_than(LIB, _deps()) else \
             list(ex.map(compile_one, _sources()))
     failed = [(s, r) for s, _, r in results if r.returncode != 0]

@@ -324,4 +324,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_torch", "tensor marshalling of
 
 }  // namespace
 
+// The torch and the Python of this build, for build.py, which finds it in the file.
+extern "C" __attribute__((used, visibility("default"))) const char pa_built_for[] = "pa_built_for{" PA_BUILT_FOR "}";
+
 PyMODINIT_FUNC PyInit__pa_torch(void) { return PyModule_Create(&module); }
