@@ -443,7 +443,9 @@ typedef enum {
   PA_ROPE_RAMP = 3    /* pairs that turn more than beta_fast times within                */
                       /* original_context stay, those below beta_slow turns are divided  */
                       /* by factor, a linear ramp over the pair index between; amplitude  */
-                      /* 1 + 0.1 ln(factor)                                              */
+                      /* 1 + 0.1 ln(factor). The ramp's ends are fractional pair indices: */
+                      /* for a model whose table rounds them to whole pairs (down and up) */
+                      /* pass that table                                                  */
 } pa_rope_scaling;
 
 /*
@@ -498,6 +500,11 @@ pa_status pa_rope_store_kvcache(void* q_out, int64_t q_out_stride, const void* q
  *  - when later rows make a scale grow, the rows already there are requantised,
  *    code' = e4m3(value(code) * old / new). A power of two only moves e4m3 exponents, so
  *    this rounds only what falls below 2^-6 of the new scale (in steps of 2^-9 of it).
+ *
+ * pa_decode_fp8_blockscale reads these pools, at head_dim 128; no entry point attends a prompt
+ * chunk to them, and rows of head_dim 64 can be appended but not attended. There is no copy of
+ * a block either (pa_copy_blocks takes bf16 pools): a caller copies its codes and its rows of
+ * both scales.
  */
 
 /*
@@ -514,7 +521,7 @@ pa_status pa_rope_store_kvcache(void* q_out, int64_t q_out_stride, const void* q
  * is copied first (copy-on-write). Rows past the new ones stay as they are. A sequence whose
  * lengths do not fit (n_new above context_lens, max_q_len or num_tokens, a context past the
  * table) is skipped, as is a block with a bad id; both are reported as PA_ERR_BAD_INDEX.
- * head_dim 64 or 128. Deterministic (no atomics).
+ * head_dim 64 or 128. The result does not depend on the order of anything (no global atomics).
  */
 pa_status pa_store_kvcache_fp8_blockscale(const void* k, int64_t k_stride, const void* v,
                                           int64_t v_stride, void* k_codes, void* v_codes,
@@ -526,7 +533,8 @@ pa_status pa_store_kvcache_fp8_blockscale(const void* k, int64_t k_stride, const
 
 /*
  * pa_rope_store_kvcache_fp8_blockscale — q_out = pa_rope(q), then
- * pa_store_kvcache_fp8_blockscale(pa_rope(k), v), in one launch and with the same bits.
+ * pa_store_kvcache_fp8_blockscale(pa_rope(k), v), in one call and with the same bits: one launch
+ * up to 8 tokens per SM, beyond that one for the queries and one for the rows, which may overlap.
  * positions int32 [num_tokens]; q, q_out and num_q_heads as in pa_rope_store_kvcache (the
  * queries of all num_tokens tokens are turned, of padding behind the last sequence too).
  * rot_dim must be a multiple of 16 (else PA_ERR_UNSUPPORTED: use the two calls).

@@ -345,7 +345,8 @@ def pa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "none",
                      factor: float = 1.0, original_context: float = 0.0, beta_fast: float = 32.0,
                      beta_slow: float = 1.0):
     """Frequency table of a rotary embedding: (list of rot_dim / 2 floats, amplitude). scaling
-    stretches it for longer contexts: "linear", "base" or "ramp" (include/pa.h)."""
+    stretches it for longer contexts: "linear", "base" or "ramp", whose ends are fractional pair
+    indices (include/pa.h)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
     table = (ctypes.c_float * max(1, int(rot_dim) // 2))()

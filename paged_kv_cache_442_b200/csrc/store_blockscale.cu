@@ -1,5 +1,6 @@
 // Append of new K/V rows to e4m3 pools that hold one scale for each (block, kv head), with
-// the rotary positions of q and k in the same launch.
+// the rotary positions of q and k in the same call (for many tokens the queries take a launch of
+// their own, beside whose end the rows' one may start).
 //
 // The scale of a (block, kv head) is the smallest power of two s >= 2^-126 with
 // max |x| <= 448 s over the rows the block has taken since its first one (position
